@@ -397,6 +397,169 @@ int ct_conv_transpose_backward_kernels(int nd, int64_t B, int64_t C_in,
                                        const char** dw_kernel);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The layers around a transposed convolution in a decoder block: a norm, the
+ * (gated) activation with 8-bit checkpoints, and a causal sequence mixer.
+ * The conventions at the top of this file hold for them too.  Matrices are
+ * given as rows of `cols` dense values, `*_stride` elements from one row to
+ * the next (the halves of a wider projection need no copy); codes and scales
+ * are dense.
+ * ---------------------------------------------------------------------------
+ */
+
+/* 8-bit storage.  A row is cut into groups of `group` (32, 64 or 128)
+ * consecutive values, the last one may be shorter; a group has one fp32 scale
+ * = max|v| * (1 / top), top = 127 (int8) or 448 (e4m3), and codes =
+ * round(v * (1 / scale)) (round to nearest even).  A group whose scale would be
+ * below the smallest normal fp32 number gets scale 0 and codes 0; a group that
+ * holds an infinity or a NaN gets scale NaN and codes 0, so that all of it
+ * reads back as NaN.  codes [rows, cols] bytes; scales [rows, ceil(cols / group)]. */
+typedef enum { CT_Q_NONE = 0, CT_Q_INT8 = 1, CT_Q_E4M3 = 2 } ct_quant;
+
+/*
+ * Root-mean-square norm of each row, the residual added first:
+ *   s = x + residual; rstd = 1 / sqrt(mean(s^2) + eps); y = s * rstd * weight
+ * in fp32, from the unrounded s.  residual, weight (ones), y, h, rstd and
+ * codes may be NULL; h receives s rounded once to the dtype (the residual
+ * stream's new value) and may be x or residual itself (same pointer and
+ * stride); y may be x or residual itself where h is NULL.
+ * quant != CT_Q_NONE writes y also as codes and
+ * scales, quantised from the unrounded y.  rstd [rows] is what the gradient
+ * needs.  weight [cols] has the dtype.
+ * Errors: CT_ERR_DTYPE, CT_ERR_SHAPE (rows < 0, cols < 1), CT_ERR_PARAM
+ * (quant, group, eps < 0 or NaN), CT_ERR_NULL, CT_ERR_ALIGN, CT_ERR_TOO_LARGE,
+ * CT_ERR_CUDA.  rows = 0 does nothing.
+ */
+int ct_rms_norm_forward(const void* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, const void* weight, void* y,
+                        int64_t y_stride, void* h, int64_t h_stride, float* rstd,
+                        void* codes, float* scales, int64_t rows, int64_t cols,
+                        float eps, int dtype, int quant, int group, void* stream);
+
+/*
+ * Gradient of ct_rms_norm_forward from h (x where there was no residual) and
+ * rstd.  With u = h * rstd and c = mean(weight * dy * u):
+ *   dx = rstd * (weight * dy - u * c) + dresidual   (also the residual's)
+ *   dw = sum over rows of dy * u
+ * dresidual (the gradient that arrives along h) and weight may be NULL, dx and
+ * dw too (not computed).  dx may be dy or dresidual itself.  dw is summed in
+ * fp32 in a fixed order and rounded once.  workspace (only used for dw):
+ * ct_rms_norm_backward_workspace_bytes bytes, 256-byte aligned, or NULL
+ * (allocated stream-ordered).  rows = 0 gives dw = 0.
+ * Errors as ct_rms_norm_forward, and CT_ERR_WORKSPACE.
+ */
+int ct_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
+                         int64_t h_stride, const float* rstd, const void* weight,
+                         const void* dresidual, int64_t dresidual_stride, void* dx,
+                         int64_t dx_stride, void* dw, void* workspace,
+                         size_t workspace_bytes, int64_t rows, int64_t cols,
+                         int dtype, void* stream);
+
+int ct_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int dtype,
+                                         size_t* bytes);
+
+/*
+ * A matrix kept in 8 bits (quant: CT_Q_INT8 or CT_Q_E4M3), and read back:
+ * y = code * scale, rounded once.  rows or cols = 0 do nothing.
+ * Errors: CT_ERR_DTYPE, CT_ERR_SHAPE, CT_ERR_PARAM, CT_ERR_NULL,
+ * CT_ERR_ALIGN, CT_ERR_TOO_LARGE, CT_ERR_CUDA.
+ */
+int ct_checkpoint_store(const void* x, int64_t x_stride, void* codes,
+                        float* scales, int64_t rows, int64_t cols, int dtype,
+                        int quant, int group, void* stream);
+int ct_checkpoint_load(const void* codes, const float* scales, void* y,
+                       int64_t y_stride, int64_t rows, int64_t cols, int dtype,
+                       int quant, int group, void* stream);
+
+/*
+ * y = act(gate) * up, or act(gate) with up = NULL (activation and alpha as in
+ * ct_conv_transpose_nd_ex), which also keeps its inputs as 8-bit checkpoints
+ * for the backward call.  y may be NULL (only the checkpoints are written) or
+ * gate or up itself.  Computed in fp32 from the inputs (not from the
+ * checkpoints), rounded once.  Errors as ct_checkpoint_store.
+ */
+int ct_checkpointed_activation_forward(const void* gate, int64_t gate_stride,
+                                       const void* up, int64_t up_stride, void* y,
+                                       int64_t y_stride, void* gate_codes,
+                                       float* gate_scales, void* up_codes,
+                                       float* up_scales, int64_t rows, int64_t cols,
+                                       int activation, float alpha, int dtype,
+                                       int quant, int group, void* stream);
+
+/*
+ * Its gradient at the values the checkpoints stand for (gate^, up^):
+ *   dgate = dy * up^ * act'(gate^), dup = dy * act(gate^), y = act(gate^) * up^
+ * (up_codes NULL: up^ = 1 and dup must be NULL).  dgate, dup and y may each be
+ * NULL (not computed); y is what a following layer's weight gradient needs and
+ * asks for no dy.  dgate or dup may be dy itself, not both.  At 0 the slope of
+ * relu is 0 and that of leaky relu 1.  Errors as ct_checkpoint_store.
+ */
+int ct_checkpointed_activation_backward(const void* dy, int64_t dy_stride,
+                                        const void* gate_codes,
+                                        const float* gate_scales,
+                                        const void* up_codes,
+                                        const float* up_scales, void* dgate,
+                                        int64_t dgate_stride, void* dup,
+                                        int64_t dup_stride, void* y,
+                                        int64_t y_stride, int64_t rows, int64_t cols,
+                                        int activation, float alpha, int dtype,
+                                        int quant, int group, void* stream);
+
+/*
+ * Causal linear attention with a decay for each head.  For each sequence and
+ * head, with decay = exp(log_decay[h]):
+ *   S_t = decay * S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * over the first lengths[b] tokens (lengths NULL: all T; values are taken into
+ * [0, T]); o is 0 after them and what q, k and v hold there is not used.
+ *   q, k [B, T, H, Dk], v, o [B, T, H, Dv] of one dtype: *_strides give the
+ *     element strides of batch, token and head, the last axis is dense.
+ *   log_decay [H] fp32, meant to be <= 0 (-infinity: only the token itself).
+ *   state_in, state_out [B, H, Dk, Dv] fp32: S before the first and after the
+ *     last token; NULL means zero, not wanted.  They may be the same buffer.
+ * T = 1 is a streaming step; T = 0 copies state_in.  S and all sums are fp32.
+ * Head sizes up to 256.
+ * workspace: ct_linear_attention_workspace_bytes bytes (backward: 0 or 1),
+ * 256-byte aligned, or NULL (allocated stream-ordered where needed).
+ * Errors: CT_ERR_DTYPE, CT_ERR_SHAPE, CT_ERR_NULL, CT_ERR_ALIGN,
+ * CT_ERR_TOO_LARGE, CT_ERR_WORKSPACE, CT_ERR_CUDA.
+ */
+int ct_linear_attention_forward(const void* q, const int64_t* q_strides,
+                                const void* k, const int64_t* k_strides,
+                                const void* v, const int64_t* v_strides, void* o,
+                                const int64_t* o_strides, const float* log_decay,
+                                const float* state_in, float* state_out,
+                                const int32_t* lengths, void* workspace,
+                                size_t workspace_bytes, int64_t B, int64_t T,
+                                int64_t H, int64_t Dk, int64_t Dv, float scale,
+                                int dtype, void* stream);
+
+/*
+ * Its gradients for upstream gradients dout ([B, T, H, Dv]) and dstate_out
+ * (NULL: zero):
+ *   dS_t = scale * q_t dout_t^T + decay * dS_{t+1}
+ *   dq_t = scale * S_t dout_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t
+ * dq, dk, dv and dstate_in (the gradient of state_in) may each be NULL.
+ * Gradients after a sequence's length are 0.  The decays are constants: they
+ * get no gradient.  dstate_in may be the buffer of dstate_out.
+ */
+int ct_linear_attention_backward(const void* q, const int64_t* q_strides,
+                                 const void* k, const int64_t* k_strides,
+                                 const void* v, const int64_t* v_strides,
+                                 const void* dout, const int64_t* do_strides,
+                                 const float* log_decay, const float* state_in,
+                                 const float* dstate_out, const int32_t* lengths,
+                                 void* dq, const int64_t* dq_strides, void* dk,
+                                 const int64_t* dk_strides, void* dv,
+                                 const int64_t* dv_strides, float* dstate_in,
+                                 void* workspace, size_t workspace_bytes, int64_t B,
+                                 int64_t T, int64_t H, int64_t Dk, int64_t Dv,
+                                 float scale, int dtype, void* stream);
+
+int ct_linear_attention_workspace_bytes(int64_t B, int64_t T, int64_t H,
+                                        int64_t Dk, int64_t Dv, int dtype,
+                                        int backward, size_t* bytes);
+
+/*
  * Returns the memory the host-buffer entry point keeps in its pool on the
  * current device to the device (the pool itself stays, empty).  The memory
  * is otherwise kept until process exit.  Host only; CT_ERR_CUDA on failure.

@@ -21,3 +21,9 @@ from .ct import (  # noqa: F401
     CT_ACT_RELU, CT_ACT_LEAKY_RELU, CT_ACT_SILU, CT_ACT_GELU, CT_ACT_TANH, CT_ACT_SIGMOID,
     CT_W_TORCH, CT_W_KDHW_CI_CO, CT_W_KDHW_CO_CI, ct_set_wait_limit_ns,
     CT_WAIT_LIMIT_DEFAULT_NS)
+from .block import (  # noqa: F401
+    CT_Q_E4M3, CT_Q_INT8, CT_Q_NONE, QUANTS, Checkpoint, CheckpointedActivationFunction,
+    LinearAttentionFunction, RmsNormFunction, checkpoint_load, checkpoint_store,
+    checkpointed_activation, checkpointed_activation_autograd, checkpointed_activation_backward,
+    linear_attention, linear_attention_autograd, linear_attention_backward, rms_norm,
+    rms_norm_autograd, rms_norm_backward)

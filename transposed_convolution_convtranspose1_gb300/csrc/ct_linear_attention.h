@@ -1,0 +1,45 @@
+// ct_linear_attention.h -- the one recurrence behind linear attention with a
+// decay and all of its gradients, and the kernels that run it.
+//
+//   M_t   = decay * M_{t-1} + mscale * x_t y_t^T          (M: Da x Db, fp32)
+//   out_t = oscale * M_t^T z_t
+//
+// forward in time over the first `length` tokens of each sequence, or
+// backward (reverse) from the last of them to the first:
+//   o  : x = k,  y = v,  z = q,  forward,  M starts from the state
+//   dq : x = v,  y = k,  z = do, forward,  M starts from the state transposed
+//   dv : x = q,  y = do, z = k,  reverse,  M starts from the last state's gradient
+//   dk : x = do, y = q,  z = v,  reverse,  M starts from that transposed
+// Backward in time the starting matrix enters the last token undecayed (it is
+// a gradient of the state after that token) and the matrix left after the
+// first token is decayed once more (it is a gradient of that token's state,
+// asked for the one before it).
+#pragma once
+
+#include "ct_internal.h"
+
+namespace ct {
+
+constexpr int kLaMaxD = 256;  // head sizes
+
+struct LaCore {
+    const void *z, *x, *y;
+    void* out;
+    int64_t zs[3], xs[3], ys[3], os[3];  // element strides of batch, token, head; the last axis is dense
+    int Da, Db;
+    const float* m_in;   // [B][H][Da][Db] ([B][H][Db][Da] if m_in_t), or null: zero
+    int m_in_t;
+    float* m_out;        // [B][H][Da][Db], or null
+    const float* log_decay;  // [H]
+    const int32_t* lengths;  // [B], or null: T each
+    float mscale, oscale;
+    int reverse;
+    int64_t B;
+    int T, H;
+    int dtype;
+};
+
+// Token by token on CUDA cores, the matrix in registers (ct_linear_attention.cu).
+cudaError_t launch_la_scan(const LaCore& c, cudaStream_t stream);
+
+}  // namespace ct

@@ -53,7 +53,12 @@ EXPORTS = ("ct_version", "ct_last_error", "ct_status_string",
            "ct_conv_transpose_backward_nd", "ct_conv_transpose_backward_workspace_bytes",
            "ct_conv_transpose_backward_kernels",
            "ct_conv_transpose_nd_ex", "ct_conv_transpose_ex_workspace_bytes",
-           "ct_set_wait_limit_ns")
+           "ct_set_wait_limit_ns",
+           "ct_rms_norm_forward", "ct_rms_norm_backward", "ct_rms_norm_backward_workspace_bytes",
+           "ct_checkpoint_store", "ct_checkpoint_load",
+           "ct_checkpointed_activation_forward", "ct_checkpointed_activation_backward",
+           "ct_linear_attention_forward", "ct_linear_attention_backward",
+           "ct_linear_attention_workspace_bytes")
 
 # Size of the static scratch behind ct_conv_transpose_nd_noalloc (CT_NOALLOC_SCRATCH_BYTES).
 CT_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -139,6 +144,27 @@ def _declare(h):
     h.ct_conv_transpose_backward_workspace_bytes.restype = ctypes.c_int
     h.ct_conv_transpose_backward_workspace_bytes.argtypes = _SHAPE_ARGS + [
         ctypes.POINTER(ctypes.c_size_t)]
+    _declare_block(h)
+
+
+def _declare_block(h):
+    """The norm, checkpoint and linear-attention entry points (block.py)."""
+    i, n, f, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+    for name, args in (
+            ("ct_rms_norm_forward", [_vp, n, _vp, n, _vp, _vp, n, _vp, n, _vp, _vp, _vp, n, n, f, i, i, i, _vp]),
+            ("ct_rms_norm_backward", [_vp, n, _vp, n, _vp, _vp, _vp, n, _vp, n, _vp, _vp, ctypes.c_size_t, n, n, i,
+                                      _vp]),
+            ("ct_rms_norm_backward_workspace_bytes", [n, n, i, sz]),
+            ("ct_checkpoint_store", [_vp, n, _vp, _vp, n, n, i, i, i, _vp]),
+            ("ct_checkpoint_load", [_vp, _vp, _vp, n, n, n, i, i, i, _vp]),
+            ("ct_checkpointed_activation_forward", [_vp, n, _vp, n, _vp, n] + [_vp] * 4 + [n, n, i, f, i, i, i, _vp]),
+            ("ct_checkpointed_activation_backward", [_vp, n] + [_vp] * 4 + [_vp, n] * 3 + [n, n, i, f, i, i, i, _vp]),
+            ("ct_linear_attention_forward", [_vp, _i64p] * 4 + [_vp] * 5 + [ctypes.c_size_t] + [n] * 5 + [f, i, _vp]),
+            ("ct_linear_attention_backward", [_vp, _i64p] * 4 + [_vp] * 4 + [_vp, _i64p] * 3 + [_vp, _vp, ctypes.c_size_t]
+             + [n] * 5 + [f, i, _vp]),
+            ("ct_linear_attention_workspace_bytes", [n] * 5 + [i, i, sz])):
+        fn = getattr(h, name)
+        fn.restype, fn.argtypes = i, args
 
 
 def lib():
@@ -492,8 +518,16 @@ class ConvTransposeFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w, bias, stride, padding, pad_lo, pad_hi, dilation, output_padding,
-                groups):
-        ctx.save_for_backward(x, w)
+                groups, checkpoint=None):
+        ctx.kept = None
+        if checkpoint is None:
+            ctx.save_for_backward(x, w)
+        else:
+            # x in 8 bits: a row is one channel of one batch element
+            from .block import checkpoint_store
+            c = checkpoint_store(x.flatten(2).flatten(0, 1), checkpoint)
+            ctx.save_for_backward(c.codes, c.scales, w)
+            ctx.kept = (c.group, x.dtype, tuple(x.shape))
         ctx.attrs = (stride, padding, pad_lo, pad_hi, dilation, output_padding, groups)
         ctx.has_bias = bias is not None
         return conv_transpose(x, w, bias, stride, padding, pad_lo, pad_hi, dilation,
@@ -501,21 +535,33 @@ class ConvTransposeFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        x, w = ctx.saved_tensors
         stride, padding, pad_lo, pad_hi, dilation, output_padding, groups = ctx.attrs
         need = tuple(n for n, flag in (("dx", ctx.needs_input_grad[0]),
                                        ("dw", ctx.needs_input_grad[1]),
                                        ("db", ctx.needs_input_grad[2] and ctx.has_bias)) if flag)
+        if ctx.kept is None:
+            x, w = ctx.saved_tensors
+        else:
+            from .block import Checkpoint, checkpoint_load
+            codes, scales, w = ctx.saved_tensors
+            group, dtype, shape = ctx.kept
+            # only dw reads x; its shape and type serve the others
+            x = (checkpoint_load(Checkpoint(codes, scales, group, dtype)).view(shape) if "dw" in need
+                 else torch.empty(shape, dtype=dtype, device=codes.device))
         dx, dw, db = conv_transpose_backward(x, w, dy.contiguous(), stride, padding, pad_lo,
                                              pad_hi, dilation, output_padding, groups, need)
-        return (dx, dw, db, None, None, None, None, None, None, None)
+        return (dx, dw, db, None, None, None, None, None, None, None, None)
 
 
 def conv_transpose_autograd(x, w, bias=None, stride=1, padding=0, pad_lo=None, pad_hi=None,
-                            dilation=1, output_padding=0, groups=1):
-    """conv_transpose that records itself for torch.autograd."""
+                            dilation=1, output_padding=0, groups=1, checkpoint=None):
+    """conv_transpose that records itself for torch.autograd.
+
+    checkpoint "int8" or "e4m3" keeps x for the weight gradient in 8 bits (half
+    the memory of a 16-bit x, a quarter of fp32's) instead of keeping x; dw is
+    then that of the kept values, dx and db are unchanged."""
     return ConvTransposeFunction.apply(x, w, bias, stride, padding, pad_lo, pad_hi, dilation,
-                                       output_padding, groups)
+                                       output_padding, groups, checkpoint)
 
 
 def _problem_ex(x, w, groups, w_layout):
