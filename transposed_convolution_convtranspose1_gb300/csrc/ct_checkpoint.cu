@@ -40,113 +40,308 @@ struct ActBwd {
     float alpha;
 };
 
-// Codes and scale of one group held four values a lane.
-template <int Q>
-__device__ __forceinline__ void keep(const float (&v)[4], unsigned amax, int n, int lane, uint8_t* codes, float* scale_out) {
-    amax = __reduce_max_sync(0xffffffffu, amax);
+// Work is cut per row into pieces: one thread's vector (rows aligned to 16
+// bytes) or one warp's 128 values (any alignment).  Piece i of the launch
+// belongs to row i / per_row; a launch covers fewer than 2^31 pieces.
+struct Pieces {
+    Divider per_row;
+    unsigned n;
+};
+
+// Forward on 16-byte vectors: a group is 4 to 32 neighbouring lanes, whose
+// maxima meet by shuffles; a row is padded to whole groups, so groups of
+// short rows share a warp.  Bound by memory: 2 bytes read and 2 + 1 written
+// (gated: 4 and 2 + 2) for an element of a 16-bit tensor.
+template <typename T, int VEC, int Q, int A>
+__global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P, Pieces W) {
+    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
+    unsigned piece;
+    const unsigned r32 = divide(i, W.per_row, &piece);
+    const int col = (int)piece * VEC;
+    const bool in = i < W.n && col < P.cols;
+    const int64_t row = r32;
+    const int lanes = P.group / VEC;
+    Vec<T, VEC> gv, uv;
+    gv.zero();
+    uv.zero();
+    if (in) {
+        gv.load(static_cast<const T*>(P.gate) + row * P.gs + col);
+        if (P.up) uv.load(static_cast<const T*>(P.up) + row * P.us + col);
+    }
+    float a[VEC], b[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        a[k] = gv.get(k);
+        b[k] = uv.get(k);
+    }
+    if (in && P.y) {
+        float o[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            o[k] = act_value<A, sizeof(T) == 2>(a[k], P.alpha);
+            if (P.up) o[k] *= b[k];
+        }
+        Vec<T, VEC> ov;
+        ov.set(o);
+        ov.store(static_cast<T*>(P.y) + row * P.ys + col);
+    }
+    unsigned amax = gv.top_bits(), bmax = uv.top_bits();
+    if constexpr (sizeof(T) == 2) {  // both inputs' maxima in one word
+        const uint32_t both = lanes_max2(amax | bmax << 16, lanes);
+        amax = both & 0xffffu;
+        bmax = both >> 16;
+    } else {
+        amax = lanes_max(amax, lanes);
+        if (P.up) bmax = lanes_max(bmax, lanes);
+    }
+    amax = Vec<T, VEC>::to_abs_bits(amax);
+    bmax = Vec<T, VEC>::to_abs_bits(bmax);
+    if (!in) return;
+    const bool first = (threadIdx.x & (lanes - 1)) == 0;
+    const int64_t at = row * P.n_groups + col / P.group;
     float scale, inv;
     group_scale<Q>(amax, scale, inv);
-    if (lane == 0) *scale_out = scale;
+    store_codes<Q, VEC>(P.gc + row * P.cols + col, a, inv);
+    if (first) P.gsc[at] = scale;
+    if (P.up) {
+        group_scale<Q>(bmax, scale, inv);
+        store_codes<Q, VEC>(P.uc + row * P.cols + col, b, inv);
+        if (first) P.usc[at] = scale;
+    }
+}
+
+// The gradient (and, without dy, reading a checkpoint back) on 16-byte
+// vectors.  Bound by memory: dy and the codes read, one or two gradients
+// written.
+template <typename T, int VEC, int Q, int A>
+__global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P, Pieces W) {
+    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= W.n) return;
+    unsigned piece;
+    const unsigned r32 = divide(i, W.per_row, &piece);
+    const int col = (int)piece * VEC;
+    const int64_t row = r32, at = row * P.n_groups + col / P.group;
+    float a[VEC], b[VEC];
+    Vec<T, VEC> dv;
+    if (P.dy) dv.load(static_cast<const T*>(P.dy) + row * P.dys + col);
+    load_codes<Q, VEC>(P.gc + row * P.cols + col, a);
+    if (P.uc) load_codes<Q, VEC>(P.uc + row * P.cols + col, b);
+    const float gsc = P.gsc[at], usc = P.uc ? P.usc[at] : 1.f;
+    float f[VEC], slope[VEC], o[VEC];
+    Vec<T, VEC> ov;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        a[k] *= gsc;
+        if (P.uc) b[k] *= usc;
+        act_both<A, sizeof(T) == 2>(a[k], P.alpha, f[k], slope[k]);
+    }
+    if (P.y) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] = P.uc ? f[k] * b[k] : f[k];
+        ov.set(o);
+        ov.store(static_cast<T*>(P.y) + row * P.ys + col);
+    }
+    if (P.dgate) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            o[k] = dv.get(k) * slope[k];
+            if (P.uc) o[k] *= b[k];
+        }
+        ov.set(o);
+        ov.store(static_cast<T*>(P.dgate) + row * P.dgs + col);
+    }
+    if (P.dup) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] = dv.get(k) * f[k];
+        ov.set(o);
+        ov.store(static_cast<T*>(P.dup) + row * P.dus + col);
+    }
+}
+
+// Maximum of each group of a warp's 128 values, slot j of every lane being
+// value j * 32 + lane: groups are 1, 2 or 4 slots.
+__device__ __forceinline__ void slot_max(unsigned (&m)[4], int group) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = __reduce_max_sync(0xffffffffu, m[j]);
+    if (group >= 64) {
+        m[0] = m[1] = max(m[0], m[1]);
+        m[2] = m[3] = max(m[2], m[3]);
+    }
+    if (group == 128) m[0] = m[1] = m[2] = m[3] = max(m[0], m[2]);
+}
+
+// Codes and scales of a warp's 128 values (n of them inside the row).
+template <int Q>
+__device__ __forceinline__ void keep(const float (&v)[4], const unsigned (&m)[4], int n, int lane, int group, uint8_t* codes,
+                                     float* scales) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int k = j * 32 + lane;
-        if (k < n) codes[k] = encode<Q>(v[j], inv);
-    }
-}
-
-// Simple form: a warp per group of a row; any size and alignment.
-template <typename T, int Q, int A>
-__global__ void __launch_bounds__(kThreads) act_fwd_groups(ActFwd P) {
-    const int lane = threadIdx.x & 31;
-    const int64_t n_work = P.rows * P.n_groups;
-    for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < n_work;
-         i += (int64_t)gridDim.x * (kThreads / 32)) {
-        const int64_t row = i / P.n_groups;
-        const int c0 = (int)(i - row * P.n_groups) * P.group, n = min(P.group, P.cols - c0);
-        const T* g = static_cast<const T*>(P.gate) + row * P.gs + c0;
-        const T* u = P.up ? static_cast<const T*>(P.up) + row * P.us + c0 : nullptr;
-        T* y = P.y ? static_cast<T*>(P.y) + row * P.ys + c0 : nullptr;
-        float a[4], b[4];
-        unsigned amax = 0, bmax = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = j * 32 + lane;
-            a[j] = b[j] = 0.f;
-            if (k < n) {
-                a[j] = to_f32(g[k]);
-                amax = max(amax, abs_bits(a[j]));
-                if (u) {
-                    b[j] = to_f32(u[k]);
-                    bmax = max(bmax, abs_bits(b[j]));
-                }
-                if (y) {
-                    const float v = act_fixed<A>(a[j], P.alpha);
-                    y[k] = from_f32<T>(u ? v * b[j] : v);
-                }
-            }
-        }
-        keep<Q>(a, amax, n, lane, P.gc + row * P.cols + c0, P.gsc + i);
-        if (u) keep<Q>(b, bmax, n, lane, P.uc + row * P.cols + c0, P.usc + i);
-    }
-}
-
-// Simple form of the gradient, and of reading a checkpoint back (no dy).
-template <typename T, int Q, int A>
-__global__ void __launch_bounds__(kThreads) act_bwd_groups(ActBwd P) {
-    const int lane = threadIdx.x & 31;
-    const int64_t n_work = P.rows * P.n_groups;
-    for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < n_work;
-         i += (int64_t)gridDim.x * (kThreads / 32)) {
-        const int64_t row = i / P.n_groups;
-        const int c0 = (int)(i - row * P.n_groups) * P.group, n = min(P.group, P.cols - c0);
-        const uint8_t* gc = P.gc + row * P.cols + c0;
-        const uint8_t* uc = P.uc ? P.uc + row * P.cols + c0 : nullptr;
-        const float gsc = P.gsc[i], usc = uc ? P.usc[i] : 1.f;
-        const T* dy = P.dy ? static_cast<const T*>(P.dy) + row * P.dys + c0 : nullptr;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = j * 32 + lane;
-            if (k >= n) continue;
-            const float a = decode<Q>(gc[k]) * gsc, b = uc ? decode<Q>(uc[k]) * usc : 1.f;
-            const float f = act_fixed<A>(a, P.alpha);
-            if (P.y) static_cast<T*>(P.y)[row * P.ys + c0 + k] = from_f32<T>(uc ? f * b : f);
-            if (!dy) continue;
-            const float d = to_f32(dy[k]);
-            if (P.dgate) {
-                const float t = d * act_slope<A>(a, P.alpha);
-                static_cast<T*>(P.dgate)[row * P.dgs + c0 + k] = from_f32<T>(uc ? t * b : t);
-            }
-            if (P.dup) static_cast<T*>(P.dup)[row * P.dus + c0 + k] = from_f32<T>(d * f);
+        float scale, inv;
+        group_scale<Q>(m[j], scale, inv);
+        if (k < n) {
+            codes[k] = encode<Q>(v[j], inv);
+            if (k % group == 0) scales[k / group] = scale;
         }
     }
 }
 
-unsigned warps_grid(int64_t work) {
-    return (unsigned)std::min<int64_t>((work + kThreads / 32 - 1) / (kThreads / 32), 1 << 20);
+// Forward for rows of any alignment: a warp takes 128 consecutive values,
+// four a lane, all loads before the first use.
+template <typename T, int Q, int A>
+__global__ void __launch_bounds__(kThreads) act_fwd_any(ActFwd P, Pieces W) {
+    const int lane = threadIdx.x & 31;
+    const unsigned i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (i >= W.n) return;
+    unsigned piece;
+    const unsigned r32 = divide(i, W.per_row, &piece);
+    const int c0 = (int)piece * 128, n = min(128, P.cols - c0);
+    const int64_t row = r32;
+    const T* g = static_cast<const T*>(P.gate) + row * P.gs + c0;
+    const T* u = P.up ? static_cast<const T*>(P.up) + row * P.us + c0 : nullptr;
+    T* y = P.y ? static_cast<T*>(P.y) + row * P.ys + c0 : nullptr;
+    float a[4], b[4];
+    unsigned amax[4], bmax[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int k = j * 32 + lane;
+        a[j] = k < n ? to_f32(g[k]) : 0.f;
+        b[j] = u && k < n ? to_f32(u[k]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int k = j * 32 + lane;
+        amax[j] = abs_bits(a[j]);
+        bmax[j] = abs_bits(b[j]);
+        if (y && k < n) {
+            const float v = act_value<A, sizeof(T) == 2>(a[j], P.alpha);
+            y[k] = from_f32<T>(u ? v * b[j] : v);
+        }
+    }
+    const int64_t at = row * P.n_groups + c0 / P.group;
+    slot_max(amax, P.group);
+    keep<Q>(a, amax, n, lane, P.group, P.gc + row * P.cols + c0, P.gsc + at);
+    if (u) {
+        slot_max(bmax, P.group);
+        keep<Q>(b, bmax, n, lane, P.group, P.uc + row * P.cols + c0, P.usc + at);
+    }
+}
+
+// The gradient for rows of any alignment.
+template <typename T, int Q, int A>
+__global__ void __launch_bounds__(kThreads) act_bwd_any(ActBwd P, Pieces W) {
+    const int lane = threadIdx.x & 31;
+    const unsigned i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (i >= W.n) return;
+    unsigned piece;
+    const unsigned r32 = divide(i, W.per_row, &piece);
+    const int c0 = (int)piece * 128, n = min(128, P.cols - c0);
+    const int64_t row = r32, at = row * P.n_groups + c0 / P.group;
+    const uint8_t* gc = P.gc + row * P.cols + c0;
+    const uint8_t* uc = P.uc ? P.uc + row * P.cols + c0 : nullptr;
+    const T* dy = P.dy ? static_cast<const T*>(P.dy) + row * P.dys + c0 : nullptr;
+    float a[4], b[4], d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int k = j * 32 + lane;
+        const bool in = k < n;
+        a[j] = in ? decode<Q>(gc[k]) * P.gsc[at + k / P.group] : 0.f;
+        b[j] = uc && in ? decode<Q>(uc[k]) * P.usc[at + k / P.group] : 1.f;
+        d[j] = dy && in ? to_f32(dy[k]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int k = j * 32 + lane;
+        if (k >= n) continue;
+        float f, slope;
+        act_both<A, sizeof(T) == 2>(a[j], P.alpha, f, slope);
+        if (P.y) static_cast<T*>(P.y)[row * P.ys + c0 + k] = from_f32<T>(f * b[j]);
+        if (P.dgate) static_cast<T*>(P.dgate)[row * P.dgs + c0 + k] = from_f32<T>(d[j] * slope * b[j]);
+        if (P.dup) static_cast<T*>(P.dup)[row * P.dus + c0 + k] = from_f32<T>(d[j] * f);
+    }
+}
+
+bool rows16(const void* p, int64_t stride, size_t eb, int64_t rows) {
+    return !p || ((uintptr_t)p % 16 == 0 && (rows <= 1 || (stride * (int64_t)eb) % 16 == 0));
+}
+
+// Rows per launch so that its pieces stay below 2^31.
+int64_t slab_rows(int per_row) { return std::max<int64_t>(1, ((1ll << 31) - 1 - kThreads) / per_row); }
+
+template <typename T, int Q, int A>
+cudaError_t launch_fwd_a(ActFwd P, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool vec = P.cols % V == 0 && rows16(P.gate, P.gs, sizeof(T), P.rows) && rows16(P.up, P.us, sizeof(T), P.rows) &&
+                     rows16(P.y, P.ys, sizeof(T), P.rows) && rows16(P.gc, 0, 1, 1) && rows16(P.uc, 0, 1, 1);
+    const int per_row = vec ? P.n_groups * (P.group / V) : (P.cols + 127) / 128;
+    const int64_t slab = slab_rows(per_row), rows = P.rows;
+    for (int64_t r = 0; r < rows; r += slab) {
+        const int64_t here = std::min(slab, rows - r);
+        const Pieces W{divider((unsigned)per_row), (unsigned)(here * per_row)};
+        if (vec) act_fwd_vec<T, V, Q, A><<<(W.n + kThreads - 1) / kThreads, kThreads, 0, s>>>(P, W);
+        else act_fwd_any<T, Q, A><<<(W.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(P, W);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        P.gate = static_cast<const T*>(P.gate) + here * P.gs;
+        if (P.up) P.up = static_cast<const T*>(P.up) + here * P.us;
+        if (P.y) P.y = static_cast<T*>(P.y) + here * P.ys;
+        P.gc += here * P.cols;
+        P.gsc += here * P.n_groups;
+        if (P.up) P.uc += here * P.cols, P.usc += here * P.n_groups;
+    }
+    return cudaSuccess;
+}
+
+template <typename T, int Q, int A>
+cudaError_t launch_bwd_a(ActBwd P, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool vec = P.cols % V == 0 && rows16(P.dy, P.dys, sizeof(T), P.rows) && rows16(P.dgate, P.dgs, sizeof(T), P.rows) &&
+                     rows16(P.dup, P.dus, sizeof(T), P.rows) && rows16(P.y, P.ys, sizeof(T), P.rows) && rows16(P.gc, 0, 1, 1) &&
+                     rows16(P.uc, 0, 1, 1);
+    const int per_row = vec ? P.cols / V : (P.cols + 127) / 128;
+    const int64_t slab = slab_rows(per_row), rows = P.rows;
+    for (int64_t r = 0; r < rows; r += slab) {
+        const int64_t here = std::min(slab, rows - r);
+        const Pieces W{divider((unsigned)per_row), (unsigned)(here * per_row)};
+        if (vec) act_bwd_vec<T, V, Q, A><<<(W.n + kThreads - 1) / kThreads, kThreads, 0, s>>>(P, W);
+        else act_bwd_any<T, Q, A><<<(W.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(P, W);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        if (P.dy) P.dy = static_cast<const T*>(P.dy) + here * P.dys;
+        if (P.dgate) P.dgate = static_cast<T*>(P.dgate) + here * P.dgs;
+        if (P.dup) P.dup = static_cast<T*>(P.dup) + here * P.dus;
+        if (P.y) P.y = static_cast<T*>(P.y) + here * P.ys;
+        P.gc += here * P.cols;
+        P.gsc += here * P.n_groups;
+        if (P.uc) P.uc += here * P.cols, P.usc += here * P.n_groups;
+    }
+    return cudaSuccess;
 }
 
 template <typename T, int Q>
 cudaError_t launch_fwd(const ActFwd& P, int act, cudaStream_t s) {
-    const unsigned grid = warps_grid(P.rows * P.n_groups);
     switch (act) {
-#define CASE(A) case A: act_fwd_groups<T, Q, A><<<grid, kThreads, 0, s>>>(P); break
-        CASE(1); CASE(2); CASE(3); CASE(4); CASE(5); CASE(6);
-        default: act_fwd_groups<T, Q, 0><<<grid, kThreads, 0, s>>>(P);
-#undef CASE
+        case 1: return launch_fwd_a<T, Q, 1>(P, s);
+        case 2: return launch_fwd_a<T, Q, 2>(P, s);
+        case 3: return launch_fwd_a<T, Q, 3>(P, s);
+        case 4: return launch_fwd_a<T, Q, 4>(P, s);
+        case 5: return launch_fwd_a<T, Q, 5>(P, s);
+        case 6: return launch_fwd_a<T, Q, 6>(P, s);
+        default: return launch_fwd_a<T, Q, 0>(P, s);
     }
-    return cudaGetLastError();
 }
 
 template <typename T, int Q>
 cudaError_t launch_bwd(const ActBwd& P, int act, cudaStream_t s) {
-    const unsigned grid = warps_grid(P.rows * P.n_groups);
     switch (act) {
-#define CASE(A) case A: act_bwd_groups<T, Q, A><<<grid, kThreads, 0, s>>>(P); break
-        CASE(1); CASE(2); CASE(3); CASE(4); CASE(5); CASE(6);
-        default: act_bwd_groups<T, Q, 0><<<grid, kThreads, 0, s>>>(P);
-#undef CASE
+        case 1: return launch_bwd_a<T, Q, 1>(P, s);
+        case 2: return launch_bwd_a<T, Q, 2>(P, s);
+        case 3: return launch_bwd_a<T, Q, 3>(P, s);
+        case 4: return launch_bwd_a<T, Q, 4>(P, s);
+        case 5: return launch_bwd_a<T, Q, 5>(P, s);
+        case 6: return launch_bwd_a<T, Q, 6>(P, s);
+        default: return launch_bwd_a<T, Q, 0>(P, s);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t run_fwd(const ActFwd& P, int act, int dtype, int quant, cudaStream_t s) {

@@ -12,6 +12,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -32,6 +33,13 @@ constexpr float kMinNormal = 1.17549435e-38f;
 // whether anything is not finite (fmaxf would drop a NaN).
 __device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// max(a, |v|) that keeps a NaN once it has met one.
+__device__ __forceinline__ float abs_max(float a, float v) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(v)));
+    return m;
+}
+
 // Scale and reciprocal scale of a group from the maximum of its abs_bits.
 // Q: CT_Q_INT8 or CT_Q_E4M3.  inv = 0 marks a group whose codes are all 0.
 template <int Q>
@@ -43,17 +51,39 @@ __device__ __forceinline__ void group_scale(unsigned amax_bits, float& scale, fl
     else inv = __frcp_rn(scale);
 }
 
-// One code.  With inv = 0 the code is 0 whatever v is (inf * 0 and NaN
-// included).
+// Rounding v * inv to an integer by adding 1.5 * 2^23: the sum's low byte is
+// the nearest integer (ties to even), for products below 2^22.  The product is
+// rounded first, as the format says; the two may not be fused.  Codes need no
+// clamp: |v| * inv exceeds 127 by a few roundings at most.  Conversion
+// instructions run at an eighth of the add's rate, and two for each element
+// were what bounded the activation's forward pass (16384 x 4096 gated bf16:
+// 146 us with them).
+__device__ __forceinline__ uint32_t int_bits(float v, float inv) {
+    return __float_as_uint(__fadd_rn(__fmul_rn(v, inv), 12582912.f));
+}
+
+// Four codes in one word; inv = 0 gives codes 0 whatever v is (infinity * 0
+// and NaN included).
+template <int Q>
+__device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
+    uint32_t c;
+    if constexpr (Q == CT_Q_INT8) {
+        const uint32_t lo = __byte_perm(int_bits(v[0], inv), int_bits(v[1], inv), 0x0040);
+        const uint32_t hi = __byte_perm(int_bits(v[2], inv), int_bits(v[3], inv), 0x0040);
+        c = __byte_perm(lo, hi, 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+        c = lo | hi << 16;
+    }
+    return inv == 0.f ? 0u : c;
+}
+
 template <int Q>
 __device__ __forceinline__ uint8_t encode(float v, float inv) {
     if (inv == 0.f) return 0;
-    if constexpr (Q == CT_Q_INT8) {
-        const int q = __float2int_rn(v * inv);
-        return (uint8_t)(int8_t)max(-127, min(127, q));
-    } else {
-        return (uint8_t)__nv_cvt_float_to_fp8(v * inv, __NV_SATFINITE, __NV_E4M3);
-    }
+    if constexpr (Q == CT_Q_INT8) return (uint8_t)int_bits(v, inv);
+    else return (uint8_t)__nv_cvt_float_to_fp8(v * inv, __NV_SATFINITE, __NV_E4M3);
 }
 
 template <int Q>
@@ -62,23 +92,213 @@ __device__ __forceinline__ float decode(uint8_t c) {
     else return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
 }
 
-// Derivative of act_fixed<A> (ct_types.cuh) at v.
-template <int A>
-__device__ __forceinline__ float act_slope(float v, float alpha) {
-    if constexpr (A == 1) return v > 0.f ? 1.f : 0.f;
-    else if constexpr (A == 2) return v >= 0.f ? 1.f : alpha;
-    else if constexpr (A == 3) {
-        const float s = 1.f / (1.f + expf(-v));
-        return s * (1.f + v * (1.f - s));
+// The four values of a word of codes (unscaled).  int8: a byte c + 128 put
+// under the exponent of 2^23 is the number 2^23 + 128 + c, again without a
+// conversion instruction.
+template <int Q>
+__device__ __forceinline__ void decode4(uint32_t c, float* v) {
+    if constexpr (Q == CT_Q_INT8) {
+        c ^= 0x80808080u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(c, 0x4b000000u, 0x7440 + i)) - 8388736.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> (16 * i)), __NV_E4M3));
+            const float2 f = __half22float2(h);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// 1 / (1 + exp(-v)).  FAST (results that are rounded to 16 bits) takes the
+// exponential and the reciprocal from the special-function unit as they are:
+// relative error below 2^-21 + |v| 2^-24, an eighth of the instructions.  Below
+// v = -88 either form gives 0 where the true value is below 1e-36.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float v) {
+    if constexpr (FAST) {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return r;
+    } else {
+        return __fdividef(1.f, 1.f + expf(-v));
+    }
+}
+
+// Activation (ct_activation codes) and its derivative at v.
+template <int A, bool FAST>
+__device__ __forceinline__ float act_value(float v, float alpha) {
+    if constexpr (A == 3) return v * sigmoid<FAST>(v);
+    else if constexpr (A == 6) return sigmoid<FAST>(v);
+    else return act_fixed<A>(v, alpha);
+}
+
+template <int A, bool FAST>
+__device__ __forceinline__ void act_both(float v, float alpha, float& f, float& slope) {
+    if constexpr (A == 1) {
+        f = v > 0.f ? v : 0.f;
+        slope = v > 0.f ? 1.f : 0.f;
+    } else if constexpr (A == 2) {
+        f = v >= 0.f ? v : alpha * v;
+        slope = v >= 0.f ? 1.f : alpha;
+    } else if constexpr (A == 3) {
+        const float s = sigmoid<FAST>(v);
+        f = v * s;
+        slope = fmaf(f, 1.f - s, s);
     } else if constexpr (A == 4) {
-        return 0.5f * (1.f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
+        const float cdf = 0.5f * (1.f + erff(v * 0.70710678118654752f));
+        f = v * cdf;
+        slope = fmaf(v * expf(-0.5f * v * v), 0.39894228040143268f, cdf);
     } else if constexpr (A == 5) {
-        const float t = tanhf(v);
-        return 1.f - t * t;
+        f = tanhf(v);
+        slope = fmaf(-f, f, 1.f);
     } else if constexpr (A == 6) {
-        const float s = 1.f / (1.f + expf(-v));
-        return s * (1.f - s);
-    } else return 1.f;
+        f = sigmoid<FAST>(v);
+        slope = f * (1.f - f);
+    } else {
+        f = v;
+        slope = 1.f;
+    }
+}
+
+// VEC consecutive elements of a row as one load or store of up to 16 bytes
+// (VEC = 1: one element), widened to fp32.
+template <typename T, int VEC>
+struct Vec {
+    static constexpr int kWords = VEC * (int)sizeof(T) >= 4 ? VEC * (int)sizeof(T) / 4 : 1;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+            else w[0] = *reinterpret_cast<const unsigned short*>(p);
+        } else {
+            static_assert(sizeof(w) == 16, "one 16-byte access");
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+            else *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else {
+            const unsigned short b = (unsigned short)(w[i >> 1] >> ((i & 1) * 16));
+            if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(b));
+            else return __uint_as_float((uint32_t)b << 16);
+        }
+    }
+    // The largest |v| as the element type's own bits (ordered, NaN on top);
+    // for 16-bit types two at a time.
+    __device__ __forceinline__ uint32_t top_bits() const {
+        uint32_t m = 0;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) m = max(m, w[i] & 0x7fffffffu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+        }
+        return m;
+    }
+    // abs_bits of the fp32 value of such bits
+    static __device__ __forceinline__ unsigned to_abs_bits(uint32_t m) {
+        if constexpr (sizeof(T) == 4) return m;
+        else if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+        else return m << 16;
+    }
+    // all VEC values at once, each rounded once
+    __device__ __forceinline__ void set(const float (&v)[VEC]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(v[i]);
+        } else if constexpr (VEC == 1) {
+            if constexpr (std::is_same<T, __half>::value) w[0] = __half_as_ushort(__float2half_rn(v[0]));
+            else w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+        }
+    }
+};
+
+// VEC codes written as one access.
+template <int Q, int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[VEC], float inv) {
+    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(p) = make_uint2(encode4<Q>(v, inv), encode4<Q>(v + 4, inv));
+    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(p) = encode4<Q>(v, inv);
+    else *p = encode<Q>(v[0], inv);
+}
+
+// VEC codes read as one access and decoded (unscaled).
+template <int Q, int VEC>
+__device__ __forceinline__ void load_codes(const uint8_t* p, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = decode<Q>(*p);
+    } else {
+        uint32_t w[2];
+        if constexpr (VEC == 8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[0] = u.x; w[1] = u.y;
+        } else w[0] = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) decode4<Q>(w[i], v + 4 * i);
+    }
+}
+
+// Quotient and remainder by a divisor known to the host, for i < 2^31: m =
+// floor(2^32 / d) + 1 gives the quotient or one more.  (d = 1: m = 0.)
+struct Divider {
+    unsigned d, m;
+};
+inline Divider divider(unsigned d) { return {d, d == 1 ? 0u : (unsigned)((1ull << 32) / d) + 1u}; }
+__device__ __forceinline__ unsigned divide(unsigned i, Divider v, unsigned* rest) {
+    if (v.m == 0) {
+        *rest = 0;
+        return i;
+    }
+    unsigned q = __umulhi(i, v.m);
+    int r = (int)(i - q * v.d);
+    if (r < 0) {
+        --q;
+        r += (int)v.d;
+    }
+    *rest = (unsigned)r;
+    return q;
+}
+
+// Both halves of a word reduced at once (two 16-bit maxima in one).
+__device__ __forceinline__ uint32_t lanes_max2(uint32_t v, int lanes) {
+    for (int o = lanes >> 1; o; o >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// Maximum over `lanes` (a power of two) neighbouring lanes.
+__device__ __forceinline__ unsigned lanes_max(unsigned v, int lanes) {
+    for (int o = lanes >> 1; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
