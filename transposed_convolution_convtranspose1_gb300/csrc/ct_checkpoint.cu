@@ -17,6 +17,7 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 2;  // vectors a thread has in flight
 
 struct ActFwd {
     const void *gate, *up;
@@ -52,109 +53,135 @@ struct Pieces {
 // maxima meet by shuffles; a row is padded to whole groups, so groups of
 // short rows share a warp.  Bound by memory: 2 bytes read and 2 + 1 written
 // (gated: 4 and 2 + 2) for an element of a 16-bit tensor.
-template <typename T, int VEC, int Q, int A>
+template <typename T, int VEC, int Q, int A, int U>
 __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P, Pieces W) {
-    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
-    unsigned piece;
-    const unsigned r32 = divide(i, W.per_row, &piece);
-    const int col = (int)piece * VEC;
-    const bool in = i < W.n && col < P.cols;
-    const int64_t row = r32;
     const int lanes = P.group / VEC;
-    Vec<T, VEC> gv, uv;
-    gv.zero();
-    uv.zero();
-    if (in) {
-        gv.load(static_cast<const T*>(P.gate) + row * P.gs + col);
-        if (P.up) uv.load(static_cast<const T*>(P.up) + row * P.us + col);
-    }
-    float a[VEC], b[VEC];
+    int64_t row[U];
+    int col[U];
+    bool in[U];
+    Vec<T, VEC> gv[U], uv[U];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-        a[k] = gv.get(k);
-        b[k] = uv.get(k);
+    for (int j = 0; j < U; ++j) {
+        const unsigned i = (blockIdx.x * U + j) * kThreads + threadIdx.x;
+        unsigned piece;
+        row[j] = divide(i, W.per_row, &piece);
+        col[j] = (int)piece * VEC;
+        in[j] = i < W.n && col[j] < P.cols;
+        gv[j].zero();
+        uv[j].zero();
+        if (in[j]) {
+            gv[j].load(static_cast<const T*>(P.gate) + row[j] * P.gs + col[j]);
+            if (P.up) uv[j].load(static_cast<const T*>(P.up) + row[j] * P.us + col[j]);
+        }
     }
-    if (in && P.y) {
-        float o[VEC];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        float a[VEC], b[VEC];
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            o[k] = act_value<A, sizeof(T) == 2>(a[k], P.alpha);
-            if (P.up) o[k] *= b[k];
+            a[k] = gv[j].get(k);
+            b[k] = uv[j].get(k);
         }
-        Vec<T, VEC> ov;
-        ov.set(o);
-        ov.store(static_cast<T*>(P.y) + row * P.ys + col);
-    }
-    unsigned amax = gv.top_bits(), bmax = uv.top_bits();
-    if constexpr (sizeof(T) == 2) {  // both inputs' maxima in one word
-        const uint32_t both = lanes_max2(amax | bmax << 16, lanes);
-        amax = both & 0xffffu;
-        bmax = both >> 16;
-    } else {
-        amax = lanes_max(amax, lanes);
-        if (P.up) bmax = lanes_max(bmax, lanes);
-    }
-    amax = Vec<T, VEC>::to_abs_bits(amax);
-    bmax = Vec<T, VEC>::to_abs_bits(bmax);
-    if (!in) return;
-    const bool first = (threadIdx.x & (lanes - 1)) == 0;
-    const int64_t at = row * P.n_groups + col / P.group;
-    float scale, inv;
-    group_scale<Q>(amax, scale, inv);
-    store_codes<Q, VEC>(P.gc + row * P.cols + col, a, inv);
-    if (first) P.gsc[at] = scale;
-    if (P.up) {
-        group_scale<Q>(bmax, scale, inv);
-        store_codes<Q, VEC>(P.uc + row * P.cols + col, b, inv);
-        if (first) P.usc[at] = scale;
+        if (in[j] && P.y) {
+            float o[VEC];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                o[k] = act_value<A, sizeof(T) == 2>(a[k], P.alpha);
+                if (P.up) o[k] *= b[k];
+            }
+            Vec<T, VEC> ov;
+            ov.set(o);
+            ov.store(static_cast<T*>(P.y) + row[j] * P.ys + col[j]);
+        }
+        unsigned amax = gv[j].top_bits(), bmax = uv[j].top_bits();
+        if constexpr (sizeof(T) == 2) {  // both inputs' maxima in one word
+            const uint32_t both = lanes_max2(amax | bmax << 16, lanes);
+            amax = both & 0xffffu;
+            bmax = both >> 16;
+        } else {
+            amax = lanes_max(amax, lanes);
+            if (P.up) bmax = lanes_max(bmax, lanes);
+        }
+        if (!in[j]) continue;
+        const bool first = (threadIdx.x & (lanes - 1)) == 0;
+        const int64_t at = row[j] * P.n_groups + col[j] / P.group;
+        float scale, inv;
+        group_scale<Q>(Vec<T, VEC>::to_abs_bits(amax), scale, inv);
+        store_codes<Q, VEC>(P.gc + row[j] * P.cols + col[j], a, inv);
+        if (first) P.gsc[at] = scale;
+        if (P.up) {
+            group_scale<Q>(Vec<T, VEC>::to_abs_bits(bmax), scale, inv);
+            store_codes<Q, VEC>(P.uc + row[j] * P.cols + col[j], b, inv);
+            if (first) P.usc[at] = scale;
+        }
     }
 }
 
 // The gradient (and, without dy, reading a checkpoint back) on 16-byte
 // vectors.  Bound by memory: dy and the codes read, one or two gradients
 // written.
-template <typename T, int VEC, int Q, int A>
+template <typename T, int VEC, int Q, int A, int U>
 __global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P, Pieces W) {
-    const unsigned i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= W.n) return;
-    unsigned piece;
-    const unsigned r32 = divide(i, W.per_row, &piece);
-    const int col = (int)piece * VEC;
-    const int64_t row = r32, at = row * P.n_groups + col / P.group;
-    float a[VEC], b[VEC];
-    Vec<T, VEC> dv;
-    if (P.dy) dv.load(static_cast<const T*>(P.dy) + row * P.dys + col);
-    load_codes<Q, VEC>(P.gc + row * P.cols + col, a);
-    if (P.uc) load_codes<Q, VEC>(P.uc + row * P.cols + col, b);
-    const float gsc = P.gsc[at], usc = P.uc ? P.usc[at] : 1.f;
-    float f[VEC], slope[VEC], o[VEC];
-    Vec<T, VEC> ov;
+    int64_t row[U];
+    int col[U];
+    bool in[U];
+    Vec<T, VEC> dv[U];
+    uint32_t gw[U][VEC / 4], uw[U][VEC / 4];
+    float gsc[U], usc[U];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-        a[k] *= gsc;
-        if (P.uc) b[k] *= usc;
-        act_both<A, sizeof(T) == 2>(a[k], P.alpha, f[k], slope[k]);
+    for (int j = 0; j < U; ++j) {
+        const unsigned i = (blockIdx.x * U + j) * kThreads + threadIdx.x;
+        unsigned piece;
+        row[j] = divide(i, W.per_row, &piece);
+        col[j] = (int)piece * VEC;
+        in[j] = i < W.n;
+        usc[j] = 1.f;
+        if (in[j]) {
+            const int64_t at = row[j] * P.n_groups + col[j] / P.group;
+            if (P.dy) dv[j].load(static_cast<const T*>(P.dy) + row[j] * P.dys + col[j]);
+            code_words<VEC>(P.gc + row[j] * P.cols + col[j], gw[j]);
+            if (P.uc) code_words<VEC>(P.uc + row[j] * P.cols + col[j], uw[j]);
+            gsc[j] = P.gsc[at];
+            if (P.uc) usc[j] = P.usc[at];
+        }
     }
-    if (P.y) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) o[k] = P.uc ? f[k] * b[k] : f[k];
-        ov.set(o);
-        ov.store(static_cast<T*>(P.y) + row * P.ys + col);
-    }
-    if (P.dgate) {
+    for (int j = 0; j < U; ++j) {
+        if (!in[j]) continue;
+        float a[VEC], b[VEC], f[VEC], slope[VEC], o[VEC];
+        Vec<T, VEC> ov;
+#pragma unroll
+        for (int k = 0; k < VEC / 4; ++k) {
+            decode4<Q>(gw[j][k], a + 4 * k);
+            if (P.uc) decode4<Q>(uw[j][k], b + 4 * k);
+        }
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            o[k] = dv.get(k) * slope[k];
-            if (P.uc) o[k] *= b[k];
+            a[k] *= gsc[j];
+            if (P.uc) b[k] *= usc[j];
+            act_both<A, sizeof(T) == 2>(a[k], P.alpha, f[k], slope[k]);
         }
-        ov.set(o);
-        ov.store(static_cast<T*>(P.dgate) + row * P.dgs + col);
-    }
-    if (P.dup) {
+        if (P.y) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) o[k] = dv.get(k) * f[k];
-        ov.set(o);
-        ov.store(static_cast<T*>(P.dup) + row * P.dus + col);
+            for (int k = 0; k < VEC; ++k) o[k] = P.uc ? f[k] * b[k] : f[k];
+            ov.set(o);
+            ov.store(static_cast<T*>(P.y) + row[j] * P.ys + col[j]);
+        }
+        if (P.dgate) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                o[k] = dv[j].get(k) * slope[k];
+                if (P.uc) o[k] *= b[k];
+            }
+            ov.set(o);
+            ov.store(static_cast<T*>(P.dgate) + row[j] * P.dgs + col[j]);
+        }
+        if (P.dup) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) o[k] = dv[j].get(k) * f[k];
+            ov.set(o);
+            ov.store(static_cast<T*>(P.dup) + row[j] * P.dus + col[j]);
+        }
     }
 }
 
@@ -266,7 +293,7 @@ bool rows16(const void* p, int64_t stride, size_t eb, int64_t rows) {
 }
 
 // Rows per launch so that its pieces stay below 2^31.
-int64_t slab_rows(int per_row) { return std::max<int64_t>(1, ((1ll << 31) - 1 - kThreads) / per_row); }
+int64_t slab_rows(int per_row) { return std::max<int64_t>(1, ((1ll << 31) - 1 - kThreads * kUnroll) / per_row); }
 
 template <typename T, int Q, int A>
 cudaError_t launch_fwd_a(ActFwd P, cudaStream_t s) {
@@ -278,7 +305,7 @@ cudaError_t launch_fwd_a(ActFwd P, cudaStream_t s) {
     for (int64_t r = 0; r < rows; r += slab) {
         const int64_t here = std::min(slab, rows - r);
         const Pieces W{divider((unsigned)per_row), (unsigned)(here * per_row)};
-        if (vec) act_fwd_vec<T, V, Q, A><<<(W.n + kThreads - 1) / kThreads, kThreads, 0, s>>>(P, W);
+        if (vec) act_fwd_vec<T, V, Q, A, kUnroll><<<(W.n + kThreads * kUnroll - 1) / (kThreads * kUnroll), kThreads, 0, s>>>(P, W);
         else act_fwd_any<T, Q, A><<<(W.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(P, W);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -303,7 +330,7 @@ cudaError_t launch_bwd_a(ActBwd P, cudaStream_t s) {
     for (int64_t r = 0; r < rows; r += slab) {
         const int64_t here = std::min(slab, rows - r);
         const Pieces W{divider((unsigned)per_row), (unsigned)(here * per_row)};
-        if (vec) act_bwd_vec<T, V, Q, A><<<(W.n + kThreads - 1) / kThreads, kThreads, 0, s>>>(P, W);
+        if (vec) act_bwd_vec<T, V, Q, A, kUnroll><<<(W.n + kThreads * kUnroll - 1) / (kThreads * kUnroll), kThreads, 0, s>>>(P, W);
         else act_bwd_any<T, Q, A><<<(W.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(P, W);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

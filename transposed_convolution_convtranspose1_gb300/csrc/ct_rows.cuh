@@ -252,19 +252,15 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[VEC], f
     else *p = encode<Q>(v[0], inv);
 }
 
-// VEC codes read as one access and decoded (unscaled).
-template <int Q, int VEC>
-__device__ __forceinline__ void load_codes(const uint8_t* p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = decode<Q>(*p);
+// VEC (4 or 8) codes read as one access.
+template <int VEC>
+__device__ __forceinline__ void code_words(const uint8_t* p, uint32_t (&w)[VEC / 4]) {
+    if constexpr (VEC == 8) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x;
+        w[1] = u.y;
     } else {
-        uint32_t w[2];
-        if constexpr (VEC == 8) {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
-            w[0] = u.x; w[1] = u.y;
-        } else w[0] = *reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) decode4<Q>(w[i], v + 4 * i);
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
 }
 
