@@ -185,3 +185,40 @@ def test_autograd_against_differences():
         want = ((f(*up) - f(*down)) / (2 * step)).item()
         terms = leaves[i].grad.double() * d
         assert abs(terms.sum().item() - want) <= 300 * E * terms.abs().sum().item() + 1e-4
+
+
+def test_f16_scores_and_states_beyond_its_range():
+    """Scores and states too large for f16 (the result is not): the heads concerned are computed again, exactly as asked."""
+    B, T, H, D = 1, 300, 3, 64
+    q, k, v, do, ld, s, ds = inputs(31, B, T, H, D, D, "f16")
+    ld = torch.tensor([0.0, -0.01, -0.5], device="cuda")
+    q[:, :, 0] *= 60
+    k[:, :, 0] *= 60         # scores of 1e5
+    v[:, :, 0] *= 2.0 ** -10
+    s[:, 1] *= 1e6           # a state of 1e6, queries that bring it back
+    q[:, :, 1] *= 1e-3
+    o, last = ct.linear_attention(q, k, v, ld, s)
+    check_attention("f16", q, k, v, ld, s, None, D ** -0.5, o, last)
+    state = s.clone()
+    o2, last2 = ct.linear_attention(q, k, v, ld, state, state_out=state)
+    assert torch.equal(o, o2) and torch.equal(last, state)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_wait_that_gives_up_is_reported(dtype):
+    """With no time to wait the tensor-core kernel stops, reports it and leaves the device usable."""
+    q, k, v, do, ld, s, _ = inputs(8, 2, 700, 2, 128, 128, dtype)
+    good = ct.linear_attention(q, k, v, ld, s)
+    torch.cuda.synchronize()
+    assert ct.ct_device_status(clear=True) == (ct.CT_OK, 0)
+    before = ct.ct_set_wait_limit_ns(0)
+    try:
+        ct.linear_attention(q, k, v, ld, s)
+        torch.cuda.synchronize()
+    finally:
+        ct.ct_set_wait_limit_ns(before)
+    rc, code = ct.ct_device_status(clear=True)
+    assert rc == ct.ct.CT_ERR_DEVICE_TIMEOUT and code != 0
+    again = ct.linear_attention(q, k, v, ld, s)
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+    assert ct.ct_device_status(clear=True) == (ct.CT_OK, 0)

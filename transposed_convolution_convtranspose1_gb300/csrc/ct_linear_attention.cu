@@ -20,12 +20,13 @@ constexpr int kTokens = 16;  // tokens staged at a time
 // registers; partial outputs are joined by two shuffles and, across the four
 // warps, through shared memory once per 16 tokens.
 template <typename T, int RX>
-__global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A) {
+__global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A, const int* only, const float* kept) {
     constexpr int D = kWarps * 4 * RX;  // rows held (>= Da)
     __shared__ __align__(16) float xs[kTokens][D];
     __shared__ __align__(16) float zs[kTokens][D];
     __shared__ __align__(16) float ys[kTokens][kCols];
     __shared__ __align__(16) float part[kWarps][kTokens][kCols];
+    __shared__ float first_gamma;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane >> 3, c4 = (lane & 7) * 4;
     const int a0 = (warp * 4 + sub) * RX, b0 = blockIdx.y * kCols;
@@ -39,6 +40,14 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A) {
     const T* y = static_cast<const T*>(A.y) + b * A.ys[0] + h * A.ys[2];
     T* out = static_cast<T*>(A.out) + b * A.os[0] + h * A.os[2];
     const int64_t msize = (int64_t)A.Da * A.Db;
+    if (only && !only[bh]) {
+        if (A.m_out)
+            for (int i = tid; i < A.Da * kCols; i += kWarps * 32) {
+                const int c = b0 + i % kCols;
+                if (c < A.Db) A.m_out[bh * msize + (int64_t)(i / kCols) * A.Db + c] = kept[bh * msize + (int64_t)(i / kCols) * A.Db + c];
+            }
+        return;
+    }
 
     float m[RX][4];
 #pragma unroll
@@ -50,6 +59,13 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A) {
             if (A.m_in && a < A.Da && c < A.Db)
                 m[i][j] = A.m_in[bh * msize + (A.m_in_t ? (int64_t)c * A.Da + a : (int64_t)a * A.Db + c)];
         }
+    // gamma is rounded, and its t-th power is off by t times that: 7e-6 of the
+    // result after 300 tokens.  So the first step of every further round of 16
+    // takes what makes the round's product exp(16 g).
+    if (tid == 0 && n > kTokens) {
+        const double e = gamma, e2 = e * e, e4 = e2 * e2, e8 = e4 * e4;
+        first_gamma = gamma > 1e-10f ? (float)(exp(16.0 * (double)A.log_decay[h]) / (e8 * e4 * e2 * e)) : gamma;
+    }
     for (int t0 = 0; t0 < n; t0 += kTokens) {
         const int nt = min(kTokens, n - t0);
         for (int i = tid; i < nt * D; i += kWarps * 32) {
@@ -65,7 +81,7 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A) {
         }
         __syncthreads();
         for (int t = 0; t < nt; ++t) {
-            const float g = A.reverse && t0 + t == 0 ? 1.f : gamma;
+            const float g = t > 0 ? gamma : t0 > 0 ? first_gamma : A.reverse ? 1.f : gamma;
             float yv[4], acc[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -118,23 +134,23 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A) {
 }
 
 template <typename T>
-cudaError_t launch_t(const LaCore& A, cudaStream_t s) {
+cudaError_t launch_t(const LaCore& A, cudaStream_t s, const int* only, const float* kept) {
     const dim3 grid((unsigned)(A.B * A.H), (unsigned)((A.Db + kCols - 1) / kCols));
-    if (A.Da <= 32) la_scan<T, 2><<<grid, kWarps * 32, 0, s>>>(A);
-    else if (A.Da <= 64) la_scan<T, 4><<<grid, kWarps * 32, 0, s>>>(A);
-    else if (A.Da <= 128) la_scan<T, 8><<<grid, kWarps * 32, 0, s>>>(A);
-    else la_scan<T, 16><<<grid, kWarps * 32, 0, s>>>(A);
+    if (A.Da <= 32) la_scan<T, 2><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
+    else if (A.Da <= 64) la_scan<T, 4><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
+    else if (A.Da <= 128) la_scan<T, 8><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
+    else la_scan<T, 16><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_la_scan(const LaCore& A, cudaStream_t s) {
+cudaError_t launch_la_scan(const LaCore& A, cudaStream_t s, const int* only, const float* kept) {
     if (A.B * A.H == 0) return cudaSuccess;
     switch (A.dtype) {
-        case CT_F32: return launch_t<float>(A, s);
-        case CT_F16: return launch_t<__half>(A, s);
-        default: return launch_t<__nv_bfloat16>(A, s);
+        case CT_F32: return launch_t<float>(A, s, only, kept);
+        case CT_F16: return launch_t<__half>(A, s, only, kept);
+        default: return launch_t<__nv_bfloat16>(A, s, only, kept);
     }
 }
 
@@ -159,6 +175,34 @@ int done(cudaError_t e, const char* what) {
     return e == cudaSuccess ? CT_OK : report_error(CT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Workspace of a call: the caller's, checked, or the call's own.
+struct Workspace {
+    void* p = nullptr;
+    bool owned = false;
+    int take(void* given, size_t bytes, size_t need, cudaStream_t s) {
+        if (need == 0) return CT_OK;
+        if (given) {
+            if (bytes < need)
+                return report_error(CT_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", bytes, need);
+            if (bad_ptr(given, 256)) return report_error(CT_ERR_ALIGN, "workspace must be 256-byte aligned");
+            p = given;
+            return CT_OK;
+        }
+        cudaError_t e = cudaMallocAsync(&p, need, s);
+        if (e != cudaSuccess) return report_error(CT_ERR_CUDA, "cudaMallocAsync(workspace): %s", cudaGetErrorString(e));
+        owned = true;
+        return CT_OK;
+    }
+    cudaError_t give_back(cudaError_t e, cudaStream_t s) {
+        const cudaError_t e2 = owned ? cudaFreeAsync(p, s) : cudaSuccess;
+        return e == cudaSuccess ? e2 : e;
+    }
+};
+
+cudaError_t launch_core(const LaCore& c, void* workspace, cudaStream_t s) {
+    return la_tc_supports(c) ? launch_la_tc(c, workspace, s) : launch_la_scan(c, s);
+}
+
 LaCore core_of(const float* log_decay, const int32_t* lengths, int64_t B, int64_t T, int64_t H, int dtype) {
     LaCore c{};
     c.log_decay = log_decay;
@@ -178,11 +222,12 @@ using namespace ct;
 
 extern "C" int ct_linear_attention_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype,
                                                    int backward, size_t* bytes) {
-    (void)backward;
+    if (backward != 0 && backward != 1) return report_error(CT_ERR_PARAM, "backward must be 0 or 1");
     if (!bytes) return report_error(CT_ERR_NULL, "bytes is NULL");
     int rc = check(B, T, H, Dk, Dv, dtype);
     if (rc != CT_OK) return rc;
-    *bytes = 0;
+    // the gradients use it one after the other
+    *bytes = la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype);
     return CT_OK;
 }
 
@@ -192,8 +237,6 @@ extern "C" int ct_linear_attention_forward(const void* q, const int64_t* q_strid
                                            float* state_out, const int32_t* lengths, void* workspace,
                                            size_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t Dk,
                                            int64_t Dv, float scale, int dtype, void* stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     int rc = check(B, T, H, Dk, Dv, dtype);
     if (rc != CT_OK) return rc;
     if (B * H == 0) return CT_OK;
@@ -209,7 +252,11 @@ extern "C" int ct_linear_attention_forward(const void* q, const int64_t* q_strid
     c.Da = (int)Dk; c.Db = (int)Dv;
     c.m_in = state_in; c.m_out = state_out;
     c.oscale = scale;
-    return done(launch_la_scan(c, (cudaStream_t)stream), "linear attention");
+    cudaStream_t s = (cudaStream_t)stream;
+    Workspace ws;
+    rc = ws.take(workspace, workspace_bytes, la_tc_supports(c) ? la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype) : 0, s);
+    if (rc != CT_OK) return rc;
+    return done(ws.give_back(launch_core(c, ws.p, s), s), "linear attention");
 }
 
 extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_strides, const void* k,
@@ -220,8 +267,6 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
                                             void* dv, const int64_t* dv_strides, float* dstate_in, void* workspace,
                                             size_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t Dk,
                                             int64_t Dv, float scale, int dtype, void* stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     int rc = check(B, T, H, Dk, Dv, dtype);
     if (rc != CT_OK) return rc;
     if (B * H == 0) return CT_OK;
@@ -234,6 +279,9 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         bad_ptr(dstate_in, 4) || bad_ptr(lengths, 4))
         return report_error(CT_ERR_ALIGN, "pointers must be aligned to their element size");
     cudaStream_t s = (cudaStream_t)stream;
+    Workspace ws;
+    rc = ws.take(workspace, workspace_bytes, la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype), s);
+    if (rc != CT_OK) return rc;
     cudaError_t e = cudaSuccess;
     if (dq && T > 0) {
         LaCore c = core_of(log_decay, lengths, B, T, H, dtype);
@@ -242,7 +290,7 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         c.Da = (int)Dv; c.Db = (int)Dk;
         c.m_in = state_in; c.m_in_t = 1;
         c.oscale = scale;
-        e = launch_la_scan(c, s);
+        e = launch_core(c, ws.p, s);
     }
     if (e == cudaSuccess && dk && T > 0) {
         LaCore c = core_of(log_decay, lengths, B, T, H, dtype);
@@ -252,7 +300,7 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         c.m_in = dstate_out; c.m_in_t = 1;
         c.mscale = scale;
         c.reverse = 1;
-        e = launch_la_scan(c, s);
+        e = launch_core(c, ws.p, s);
     }
     // last, because dstate_in may be dstate_out's own buffer
     if (e == cudaSuccess && ((dv && T > 0) || dstate_in)) {
@@ -264,7 +312,7 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         c.m_in = dstate_out; c.m_out = dstate_in;
         c.mscale = scale;
         c.reverse = 1;
-        e = launch_la_scan(c, s);
+        e = launch_core(c, ws.p, s);
     }
-    return done(e, "linear attention backward");
+    return done(ws.give_back(e, s), "linear attention backward");
 }

@@ -39,7 +39,20 @@ struct LaCore {
     int dtype;
 };
 
-// Token by token on CUDA cores, the matrix in registers (ct_linear_attention.cu).
-cudaError_t launch_la_scan(const LaCore& c, cudaStream_t stream);
+// Sequences of at most this many tokens go token by token.
+constexpr int kLaScanTokens = 32;
+
+// Token by token on CUDA cores, the matrix in registers
+// (ct_linear_attention.cu).  With `only` ([B * H]) the heads whose flag is 0
+// are left alone but for m_out, which is copied from `kept`.
+cudaError_t launch_la_scan(const LaCore& c, cudaStream_t stream, const int* only = nullptr, const float* kept = nullptr);
+
+// In chunks on the tensor cores (ct_linear_attention_tc.cu): 16-bit types,
+// head sizes up to 128, tensors that TMA can address.
+bool la_tc_fits(int64_t T, int64_t Dk, int64_t Dv, int dtype);
+bool la_tc_supports(const LaCore& c);
+size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype);
+cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t stream);
+cudaError_t la_error_word(unsigned int* v, bool clear);
 
 }  // namespace ct

@@ -1,0 +1,792 @@
+// ct_linear_attention_tc.cu -- the recurrence of ct_linear_attention.h in
+// chunks of 128 tokens on the tensor cores (16-bit inputs, head sizes up to
+// 128), for prompts and gradients.
+//
+// With the chunk's rows Z, X (128 x Da), Y (128 x Db), a row i's distance
+// d(i, j) >= 0 to the rows it sees, and M the matrix before the chunk:
+//   S   = Z X^T                          128 x 128
+//   P   = S * decay^d(i,j) * mscale * oscale, 0 where j is not seen by i
+//   out = P Y + (oscale * decay^w(i)) * (Z M)
+//   M  <- decay^e M + (mscale * decay^f(j) x_j)^T Y
+// forward in time (n rows in the chunk): d = i - j, w = i + 1, f = n - 1 - j,
+// e = n; backward: d = j - i, w = n - i, f = j, e = n, one less in w and e for
+// the chunk that holds the sequence's last token.
+//
+// All four products are tcgen05 MMAs with fp32 accumulators in TMEM, 16-bit
+// operands.  S is exact in its operands.  P, M and the decayed x are fp32
+// values, and each enters as hi + lo, two 16-bit numbers, in two MMAs: with
+// one rounding each, out's error would be 1.4 to 1.7 times that of rounding
+// out itself, and the fp32 state's 2^-9.  P and x enter from TMEM (P over S,
+// in place), M from shared memory.
+//
+// One CTA per sequence, head and segment walks its chunks in order:
+//   warps 0-7   S -> P, and out: TMEM row = token, two halves of the columns
+//   warps 8-11  decayed x (TMEM row = column of X), then the scaling of Z M
+//   warps 12-15 M: fp32 -> hi, lo in shared memory, times decay^e in TMEM
+//   warp 16     TMA loads; warp 17 MMA issue; warp 18 TMA stores
+// so that the tensor cores run one product while the others are prepared.
+// Bound by memory at full occupancy: 4 x 128 x D x 2 bytes a chunk (5650
+// cycles of the SM's share of the copy rate at D = 128) against 3600 cycles of
+// MMAs.
+//
+// Few heads and long sequences: a sequence is cut into segments.  A first
+// launch forms each segment's own sum (the last line above from M = 0), a
+// small kernel chains them into the matrix before each segment, and the main
+// launch runs all segments at once.
+#include <algorithm>
+#include <cstring>
+
+#include "ct_linear_attention.h"
+#include "ct_tcgen05.cuh"
+#include "ct_types.cuh"
+
+namespace ct {
+namespace {
+
+using namespace tcg;
+
+constexpr int kC = 128;            // tokens of a chunk
+constexpr int kLaThreads = 19 * 32;
+constexpr uint32_t kTmemP = 0, kTmemX = 128, kTmemO = 256, kTmemM = 384;
+constexpr float kF16Max = 65504.f;
+
+struct LaTcParams {
+    CUtensorMap tz, tx, ty, to;  // (D, T, H, B), boxes of 64 columns x 128 tokens
+    void* out;
+    int64_t os[3];
+    const float* m_in;           // before segment 0 of the walk, or per segment
+    int m_in_t, m_in_seg;        // transposed; one for each segment ([seg][bh][Da][Db])
+    float* m_out;                // after the walk of a segment ([seg][bh])
+    int final;                   // m_out is the walk's result, not a segment's own sum
+    const float* log_decay;
+    const int32_t* lengths;
+    int* flags;                  // f16: [bh], set where a value left f16's range
+    float mscale, oscale;
+    int reverse, T, H, Da, Db, BH;
+    int seg_tokens, segs;
+    uint32_t idesc_s, idesc_n;   // N = 128, B K-major; N = DB, B MN-major
+    uint64_t wait_ns;
+};
+
+template <int DA, int DB>
+struct LaShape {
+    static constexpr int kD = DA > DB ? DA : DB;
+    static constexpr uint32_t kZ = 256 * kD;     // also out's staging
+    static constexpr uint32_t kX = 256 * DA, kY = 256 * DB, kM = 2 * DA * DB;
+    static constexpr uint32_t oZ = 0, oX = 2 * kZ, oY = oX + kX, oM = oY + 2 * kY;
+    static constexpr uint32_t kBytes = oM + 2 * kM;
+    static constexpr size_t kSmem = kBytes + 1024;
+};
+
+// MN-major operand, 128-byte swizzle: rows of 64 MN elements per K index,
+// 8-row groups 1024 bytes apart, `block` bytes between blocks of 64.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(block >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// D (+)= A B with A (16-bit, two consecutive K in a column) in TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 lanes x 16 columns: thread i holds lanes i / 4 and i / 4 + 8, columns
+// i % 4 of every four (the layout of a transposed ldmatrix of 16-bit pairs).
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed.
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// One arrival for the warp, after what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
+}
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Two fp32 values as one word of two T.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// v = hi + lo to within U^2 |v|, each half a T.
+template <typename T>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack2<T>(a, b);
+    const float2 h = unpack2<T>(hi);
+    lo = pack2<T>(a - h.x, b - h.y);
+}
+
+template <typename T, int DA, int DB, bool STATE>
+__global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcParams P) {
+    using Sh = LaShape<DA, DB>;
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    // f16 scores and decayed x are kept 16 and 64 times their size: the lo
+    // parts' steps then are 2^-28 and 2^-30, the ranges 4094 and 1023; beyond
+    // them the flag has the head done again
+    constexpr float kUp = kHalf ? 16.f : 1.f, kUpX = kHalf ? 64.f : 1.f;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ uint64_t z_full[2], x_full, y_full[2], z_free[2], x_free, y_free[2];
+    __shared__ uint64_t s_ready, zm_ready, zm_done, p_done, x_done, m_done, o_ready, m_ready, o_free, staged, drain_bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    __shared__ float tab[2 * kC];   // tab[kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j
+    __shared__ float pw[kC + 2];    // decay^k
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bh = (int)(blockIdx.x % (unsigned)P.BH), seg = (int)(blockIdx.x / (unsigned)P.BH);
+    const int b = bh / P.H, h = bh % P.H;
+    const int len = P.lengths ? max(0, min(P.T, P.lengths[b])) : P.T;
+    const int s0 = seg * P.seg_tokens, s1 = min(P.T, s0 + P.seg_tokens);
+    const int n_tok = max(0, min(len, s1) - s0);
+    const int n_chunks = (n_tok + kC - 1) / kC;
+    const int64_t msize = (int64_t)P.Da * P.Db;
+    // the walk's first chunk holds the sequence's last token: its matrix is
+    // that token's own gradient, undecayed
+    const bool holds_end = P.reverse && n_tok > 0 && s0 + n_tok == len;
+
+    // tokens after the sequence's length: out = 0 (whole chunks of them; the
+    // last chunk's own are written with it)
+    if (!STATE && P.out) {
+        const int from = s0 + n_chunks * kC;
+        const int64_t rows = s1 - from;
+        T* out = static_cast<T*>(P.out) + b * P.os[0] + h * P.os[2];
+        for (int64_t i = threadIdx.x; i < rows * P.Db; i += kLaThreads) out[(from + i / P.Db) * P.os[1] + i % P.Db] = from_f32<T>(0.f);
+    }
+    const float* m_in = P.m_in ? P.m_in + (P.m_in_seg ? ((int64_t)seg * P.BH + bh) * msize : bh * msize) : nullptr;
+    float* m_out = P.m_out ? P.m_out + ((int64_t)seg * P.BH + bh) * msize : nullptr;
+    if (n_chunks == 0) {  // the same for every thread
+        if (m_out)
+            for (int64_t i = threadIdx.x; i < msize; i += kLaThreads)
+                m_out[i] = m_in ? (P.m_in_t ? m_in[(i % P.Db) * P.Da + i / P.Db] : m_in[i]) : 0.f;
+        return;
+    }
+
+    const float g = fmaxf(P.log_decay[h], -1e30f);
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&z_full[i]), 1);
+            mbar_init(smem_u32(&y_full[i]), 1);
+            mbar_init(smem_u32(&z_free[i]), 1);
+            mbar_init(smem_u32(&y_free[i]), 1);
+        }
+        mbar_init(smem_u32(&x_full), 1);
+        mbar_init(smem_u32(&x_free), STATE ? 4 : 5);
+        mbar_init(smem_u32(&s_ready), 1);
+        mbar_init(smem_u32(&zm_ready), 1);
+        mbar_init(smem_u32(&zm_done), 4);
+        mbar_init(smem_u32(&p_done), 8);
+        mbar_init(smem_u32(&x_done), 4);
+        mbar_init(smem_u32(&m_done), 4);
+        mbar_init(smem_u32(&o_ready), 1);
+        mbar_init(smem_u32(&m_ready), 1);
+        mbar_init(smem_u32(&o_free), 8);
+        mbar_init(smem_u32(&staged), 8);
+        mbar_init(smem_u32(&drain_bar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    if (threadIdx.x < kC + 1) pw[threadIdx.x] = expf((float)threadIdx.x * g);
+    for (int i = threadIdx.x; i < 2 * kC; i += kLaThreads) {
+        const int d = P.reverse ? i - (kC - 1) : (kC - 1) - i;
+        tab[i] = d < 0 ? 0.f : expf((float)d * g) * (P.mscale * P.oscale * kUp);
+    }
+    if (warp == 17) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    auto chunk_at = [&](int c) { return P.reverse ? n_chunks - 1 - c : c; };
+    auto rows_of = [&](int k) { return min(kC, n_tok - k * kC); };
+    auto waits = [&](uint64_t& bar, int parity, unsigned code) {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)parity & 1u, code, &abort_flag, P.wait_ns));
+    };
+
+    if (warp < 8) {
+        // ----------------------------------------------------------- P, out
+        if constexpr (!STATE) {
+            const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+            [[maybe_unused]] float top = 0.f;
+            for (int c = 0; c < n_chunks; ++c) {
+                const int n = rows_of(chunk_at(c));
+                if (!waits(s_ready, c, kErrEpilogue)) break;
+                tc_fence_after();
+                float v[2][32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) tmem_ld32(lane_base + kTmemP + half * 64 + q * 32, v[q]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int j0 = half * 64 + q * 32;
+                    uint32_t hi[16], lo[16];
+                    const float* f = tab + (kC - 1) + j0 - row;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[q][i] *= f[i];
+                    if (n < kC)  // rows after the end hold anything, NaN included
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (row >= n || j0 + i >= n || (P.reverse ? j0 + i < row : j0 + i > row)) v[q][i] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        split2<T>(v[q][2 * i], v[q][2 * i + 1], hi[i], lo[i]);
+                        if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[q][2 * i]), fabsf(v[q][2 * i + 1])));
+                    }
+                    tmem_st16(lane_base + kTmemP + j0, hi);
+                    tmem_st16(lane_base + kTmemP + j0 + 16, lo);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(p_done, lane);
+
+                if (!waits(o_ready, c, kErrEpilogue)) break;
+                tc_fence_after();
+                const uint32_t stage = base + Sh::oZ + (c & 1) * Sh::kZ;
+#pragma unroll
+                for (int q = 0; q < DB / 64; ++q) tmem_ld32(lane_base + kTmemO + half * (DB / 2) + q * 32, v[q]);
+                tmem_ld_wait();
+                tc_fence_before();
+                warp_arrive(o_free, lane);
+#pragma unroll
+                for (int q = 0; q < DB / 64; ++q) {
+                    const int col = half * (DB / 2) + q * 32;
+                    const uint32_t at = stage + (col / 64) * 16384u + row * 128u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = row < n ? pack2<T>(v[q][8 * k + 2 * i] * (1.f / kUp), v[q][8 * k + 2 * i + 1] * (1.f / kUp)) : 0u;
+                        sts128(at + ((((col & 63) >> 3) + k) ^ (row & 7)) * 16u, u[0], u[1], u[2], u[3]);
+                    }
+                }
+                fence_async_smem();
+                warp_arrive(staged, lane);
+            }
+            if constexpr (kHalf)
+                if (!(top <= kF16Max)) P.flags[bh] = 1;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------- decayed x, scaling of Z M
+        const int w4 = warp & 3;
+        const bool fed = w4 * 32 < DA;  // the others' rows no column of X feeds
+        [[maybe_unused]] float top = 0.f;
+        if (!fed) {
+            uint32_t zero[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tmem_st16(lane_base + kTmemX + i * 16, zero);
+            tmem_st_wait();
+        }
+        // ldmatrix: lanes 0-7, 8-15, 16-23, 24-31 point at the rows of the
+        // matrices (x columns 0-7 | 8-15) x (tokens 0-7), then tokens 8-15
+        const uint32_t xs = base + Sh::oX + (uint32_t)(w4 >> 1) * 16384u + ((lane & 7) + (lane >> 4) * 8) * 128u;
+        const uint32_t ch = (uint32_t)(w4 & 1) * 4 + ((lane >> 3) & 1);
+        for (int c = 0; c < n_chunks; ++c) {
+            const int n = rows_of(chunk_at(c));
+            if (!waits(x_full, c, kErrEpilogue)) break;
+            bool ok = true;
+            if (fed) {
+#pragma unroll 1
+                for (int blk = 0; blk < 8 && ok; ++blk) {
+                    const int j0 = (blk >> 1) * 32, ah = blk & 1;  // 32 tokens x 16 columns of x
+                    uint32_t x[8], hi[8], lo[8];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) ldsm4_trans(xs + (j0 + 16 * k) * 128u + (((ch + ah * 2) ^ (lane & 7)) << 4), x + 4 * k);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {  // tokens j0 + 8 m + 2 (lane % 4), + 1
+                        const int j = j0 + 8 * m + 2 * (lane & 3);
+                        float f0 = pw[P.reverse ? j : max(n - 1 - j, 0)], f1 = pw[P.reverse ? j + 1 : max(n - 2 - j, 0)];
+                        f0 *= P.mscale * kUpX;
+                        f1 *= P.mscale * kUpX;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float2 v = unpack2<T>(x[2 * m + r]);
+                            v.x = j < n ? v.x * f0 : 0.f;
+                            v.y = j + 1 < n ? v.y * f1 : 0.f;
+                            split2<T>(v.x, v.y, hi[2 * m + r], lo[2 * m + r]);
+                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        }
+                    }
+                    // the MMAs of the chunk before have read these places
+                    if (blk == 0 && c > 0) {
+                        ok = waits(m_ready, c - 1, kErrEpilogue);
+                        tc_fence_after();
+                    }
+                    const uint32_t at = lane_base + ((uint32_t)(ah * 16) << 16) + kTmemX + j0;
+                    tmem_st_16x16(at, hi);
+                    tmem_st_16x16(at + 16, lo);
+                }
+                tmem_st_wait();
+            }
+            if (!ok) break;
+            warp_arrive(x_free, lane);
+            if (n < kC) {  // rows of Y after the end meet factors of 0: they must be finite
+                if (!waits(y_full[c & 1], c >> 1, kErrEpilogue)) break;
+                const uint32_t ys = base + Sh::oY + (c & 1) * Sh::kY;
+                for (int i = threadIdx.x - 256; i < (kC - n) * 8 * (DB / 64); i += 128) {
+                    const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
+                    sts128(ys + blk * 16384u + (uint32_t)(n + r / 8) * 128u + (uint32_t)(r % 8) * 16u, 0, 0, 0, 0);
+                }
+                fence_async_smem();
+            }
+            tc_fence_before();
+            warp_arrive(x_done, lane);
+            if constexpr (!STATE) {
+                if (!waits(zm_ready, c, kErrEpilogue)) break;
+                tc_fence_after();
+                const int row = w4 * 32 + lane, w = P.reverse ? n - row - (holds_end && c == 0 ? 1 : 0) : row + 1;
+                const float f = row < n ? pw[w] * P.oscale * kUp : 0.f;
+#pragma unroll 1
+                for (int q = 0; q < DB / 64; ++q) {
+                    const uint32_t at = lane_base + kTmemO + q * 64;
+                    float v[2][32];
+                    tmem_ld32(at, v[0]);
+                    tmem_ld32(at + 32, v[1]);
+                    tmem_ld_wait();
+                    uint32_t u[2][32];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) u[k][i] = row < n ? __float_as_uint(v[k][i] * f) : 0u;
+                        tmem_st16(at + k * 32, u[k]);
+                        tmem_st16(at + k * 32 + 16, u[k] + 16);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(zm_done, lane);
+            }
+        }
+        if constexpr (kHalf)
+            if (!(top <= kF16Max)) P.flags[bh] = 1;
+    } else if (warp < 16) {
+        // -------------------------------------------------------------- M
+        const int a = (warp & 3) * 32 + lane;
+        [[maybe_unused]] float top = 0.f;
+        for (int c = 0; c <= n_chunks; ++c) {
+            if (c > 0) {
+                if (!waits(m_ready, c - 1, kErrEpilogue)) break;
+                tc_fence_after();
+            }
+            const int n = c < n_chunks ? rows_of(chunk_at(c)) : 0;
+            const float f = c < n_chunks ? pw[n - (holds_end && c == 0 ? 1 : 0)] * kUpX : 1.f;
+            const float last = P.reverse && P.final ? pw[1] : 1.f;
+#pragma unroll 1
+            for (int q = 0; q < DB / 64; ++q) {
+                float v[64];
+                if (c == 0) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        const int col = q * 64 + i;
+                        v[i] = 0.f;
+                        if (m_in && a < P.Da && col < P.Db) v[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + a : (int64_t)a * P.Db + col];
+                    }
+                } else {
+                    tmem_ld32(lane_base + kTmemM + q * 64, v);
+                    tmem_ld32(lane_base + kTmemM + q * 64 + 32, v + 32);
+                    tmem_ld_wait();
+                    if constexpr (kHalf)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i] *= 1.f / kUpX;
+                }
+                if (c == n_chunks) {
+                    if (m_out && a < P.Da)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (q * 64 + i < P.Db) m_out[(int64_t)a * P.Db + q * 64 + i] = v[i] * last;
+                    continue;
+                }
+                if (!STATE && a < DA) {
+                    const uint32_t at = base + Sh::oM + (uint32_t)q * (DA * 128u) + (uint32_t)a * 128u;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            split2<T>(v[8 * k + 2 * i], v[8 * k + 2 * i + 1], hi[i], lo[i]);
+                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[8 * k + 2 * i]), fabsf(v[8 * k + 2 * i + 1])));
+                        }
+                        const uint32_t o = ((uint32_t)k ^ (uint32_t)(a & 7)) * 16u;
+                        sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
+                        sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[16 * k + i] * f);
+                    tmem_st16(lane_base + kTmemM + q * 64 + k * 16, u);
+                }
+            }
+            if (c == n_chunks) break;
+            tmem_st_wait();
+            if (!STATE) fence_async_smem();
+            tc_fence_before();
+            warp_arrive(m_done, lane);
+        }
+        if constexpr (kHalf)
+            if (!(top <= kF16Max)) P.flags[bh] = 1;
+    } else if (warp == 16) {
+        // ------------------------------------------------------- TMA loads
+        if (lane == 0) {
+            int nz = 0, ny = 0, nx = 0;  // fills issued
+            bool ok = true;
+            for (int c = 0; c < n_chunks; ++c) {
+                const int t0 = s0 + chunk_at(c) * kC, s = c & 1;
+                if (!STATE) {
+                    ok = c < 2 || mbar_wait(smem_u32(&z_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
+                    if (!ok) break;
+                    mbar_expect_tx(smem_u32(&z_full[s]), 256 * DA);
+                    for (int k = 0; k < DA / 64; ++k)
+                        tma_load_4d(base + Sh::oZ + s * Sh::kZ + k * 16384u, &P.tz, smem_u32(&z_full[s]), k * 64, t0, h, b);
+                    ++nz;
+                }
+                ok = c < 2 || mbar_wait(smem_u32(&y_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
+                if (!ok) break;
+                mbar_expect_tx(smem_u32(&y_full[s]), 256 * DB);
+                for (int k = 0; k < DB / 64; ++k)
+                    tma_load_4d(base + Sh::oY + s * Sh::kY + k * 16384u, &P.ty, smem_u32(&y_full[s]), k * 64, t0, h, b);
+                ++ny;
+                ok = c < 1 || mbar_wait(smem_u32(&x_free), (c - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
+                if (!ok) break;
+                mbar_expect_tx(smem_u32(&x_full), 256 * DA);
+                for (int k = 0; k < DA / 64; ++k)
+                    tma_load_4d(base + Sh::oX + k * 16384u, &P.tx, smem_u32(&x_full), k * 64, t0, h, b);
+                ++nx;
+            }
+            if (!ok) {
+                // what was issued must land before the CTA exits: the last
+                // fill of each slot
+                for (int i = max(0, nz - 2); i < nz; ++i) mbar_drain(smem_u32(&z_full[i & 1]), (i >> 1) & 1);
+                for (int i = max(0, ny - 2); i < ny; ++i) mbar_drain(smem_u32(&y_full[i & 1]), (i >> 1) & 1);
+                if (nx > 0) mbar_drain(smem_u32(&x_full), (nx - 1) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 17) {
+        // ------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            auto wait1 = [&](uint64_t& bar, int parity) {
+                return mbar_wait(smem_u32(&bar), (uint32_t)parity & 1u, kErrMma, &abort_flag, P.wait_ns);
+            };
+            for (int c = 0; c < n_chunks; ++c) {
+                const int s = c & 1;
+                const uint32_t zs = base + Sh::oZ + s * Sh::kZ, xs = base + Sh::oX, ys = base + Sh::oY + s * Sh::kY;
+                if constexpr (!STATE) {
+                    if (!wait1(z_full[s], c >> 1) || !wait1(x_full, c)) break;
+                    // P of the chunk before has been multiplied: its place takes S
+                    if (c > 0 && !wait1(o_ready, c - 1)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < DA / 16; ++k) {
+                        const uint32_t o = (k / 4) * 16384u;
+                        mma_f16(tmem + kTmemP, smem_desc_sw128(zs + o) + 2 * (k & 3), smem_desc_sw128(xs + o) + 2 * (k & 3), P.idesc_s,
+                                k > 0);
+                    }
+                    mma_commit(smem_u32(&s_ready));
+                    mma_commit(smem_u32(&x_free));
+                    if (!wait1(m_done, c)) break;
+                    if (c > 0 && !wait1(o_free, c - 1)) break;
+                    tc_fence_after();
+                    const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
+#pragma unroll
+                    for (int k = 0; k < DA / 16; ++k) {
+                        const uint64_t ad = smem_desc_sw128(zs + (k / 4) * 16384u) + 2 * (k & 3);
+                        mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
+                        mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
+                    }
+                    mma_commit(smem_u32(&zm_ready));
+                } else {
+                    if (!wait1(m_done, c)) break;
+                }
+                if (!wait1(x_done, c) || !wait1(y_full[s], c >> 1)) break;
+                tc_fence_after();
+                const uint64_t yd = desc_mn(ys, 16384);
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k) {
+                    const uint32_t xa = tmem + kTmemX + (k / 2) * 32 + (k & 1) * 8;
+                    mma_ts(tmem + kTmemM, xa, yd + 128 * k, P.idesc_n, 1);
+                    mma_ts(tmem + kTmemM, xa + 16, yd + 128 * k, P.idesc_n, 1);
+                }
+                mma_commit(smem_u32(&m_ready));
+                if constexpr (!STATE) {
+                    if (!wait1(zm_done, c) || !wait1(p_done, c)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k) {
+                        const uint32_t pa = tmem + kTmemP + (k / 2) * 32 + (k & 1) * 8;
+                        mma_ts(tmem + kTmemO, pa, yd + 128 * k, P.idesc_n, 1);
+                        mma_ts(tmem + kTmemO, pa + 16, yd + 128 * k, P.idesc_n, 1);
+                    }
+                    mma_commit(smem_u32(&o_ready));
+                }
+                mma_commit(smem_u32(&y_free[s]));
+            }
+            // no MMA may be in flight when TMEM is released
+            mma_commit(smem_u32(&drain_bar));
+            mbar_drain(smem_u32(&drain_bar), 0);
+        }
+        __syncwarp();
+    } else if (!STATE) {
+        // ------------------------------------------------------ TMA stores
+        if (lane == 0) {
+            for (int c = 0; c < n_chunks; ++c) {
+                if (!mbar_wait(smem_u32(&staged), c & 1, kErrEpilogue, &abort_flag, P.wait_ns)) break;
+                const int t0 = s0 + chunk_at(c) * kC;
+                for (int k = 0; k < DB / 64; ++k)
+                    if (k * 64 < P.Db) tma_store_4d(&P.to, base + Sh::oZ + (c & 1) * Sh::kZ + k * 16384u, k * 64, t0, h, b);
+                bulk_wait_read_all();
+                mbar_arrive(smem_u32(&z_free[c & 1]));
+            }
+            bulk_wait_all();
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 17)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// The matrix before each segment from the segments' own sums, in place:
+// cur <- decay^n cur + sum, element by element along the walk; the last one is
+// the walk's result.
+__global__ void __launch_bounds__(256) la_chain(float* sums, const float* m_in, int m_in_t, float* m_out, const float* log_decay,
+                                                const int32_t* lengths, int reverse, int T, int H, int Da, int Db, int BH,
+                                                int seg_tokens, int segs) {
+    const int64_t msize = (int64_t)Da * Db, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= msize * BH) return;
+    const int bh = (int)(i / msize);
+    const int64_t e = i % msize;
+    const int len = lengths ? max(0, min(T, lengths[bh / H])) : T;
+    const float g = fmaxf(log_decay[bh % H], -1e30f);
+    float cur = m_in ? m_in[bh * msize + (m_in_t ? (e % Db) * Da + e / Db : e)] : 0.f;
+    for (int k = 0; k < segs; ++k) {
+        const int seg = reverse ? segs - 1 - k : k, s0 = seg * seg_tokens;
+        const int n = max(0, min(len, min(T, s0 + seg_tokens)) - s0);
+        float* at = sums + seg * (int64_t)BH * msize + i;
+        const float sum = *at;
+        *at = cur;
+        if (n > 0) cur = fmaf(expf((float)(n - (reverse && s0 + n == len ? 1 : 0)) * g), cur, sum);
+    }
+    if (m_out) m_out[i] = reverse && len > 0 ? expf(g) * cur : cur;
+}
+
+bool map_tensor(CUtensorMap* m, const LaCore& c, const void* p, const int64_t (&st)[3], int D) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)c.T, (cuuint64_t)c.H, (cuuint64_t)c.B};
+    // an axis of one element may have any stride
+    const cuuint64_t strides[3] = {c.T > 1 ? (cuuint64_t)st[1] * 2 : 256, c.H > 1 ? (cuuint64_t)st[2] * 2 : 256,
+                                   c.B > 1 ? (cuuint64_t)st[0] * 2 : 256};
+    const cuuint32_t box[4] = {64, (cuuint32_t)kC, 1, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, c.dtype == CT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+               const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether TMA can read (or write) the tensor where it is.
+bool tma_ok(const LaCore& c, const void* p, const int64_t (&st)[3]) {
+    const int64_t n[3] = {c.B, c.T, c.H};
+    if ((uintptr_t)p % 16 != 0) return false;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] <= 0 || st[i] % 8 != 0 || st[i] >= (1ll << 38))) return false;
+    return true;
+}
+
+template <typename T, int DA, int DB, bool STATE>
+cudaError_t launch_k(const LaTcParams& P, cudaStream_t s) {
+    auto k = la_chunks<T, DA, DB, STATE>;
+    constexpr int bytes = (int)LaShape<DA, DB>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)(P.BH * P.segs), kLaThreads, bytes, s>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename T, bool STATE>
+cudaError_t launch_d(const LaTcParams& P, cudaStream_t s) {
+    if (P.Da <= 64) return P.Db <= 64 ? launch_k<T, 64, 64, STATE>(P, s) : launch_k<T, 64, 128, STATE>(P, s);
+    return P.Db <= 64 ? launch_k<T, 128, 64, STATE>(P, s) : launch_k<T, 128, 128, STATE>(P, s);
+}
+
+template <bool STATE>
+cudaError_t launch_t(const LaTcParams& P, int dtype, cudaStream_t s) {
+    return dtype == CT_BF16 ? launch_d<__nv_bfloat16, STATE>(P, s) : launch_d<__half, STATE>(P, s);
+}
+
+// Segments of a sequence, and the tokens of one: as many as fill the GPU once
+// with one CTA each, of at least four chunks (a segment costs a second read of
+// X and Y and a chain step).
+void split(int64_t B, int64_t T, int64_t H, int sm_count, int* segs, int* tokens) {
+    const int64_t chunks = (T + kC - 1) / kC;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(sm_count / std::max<int64_t>(1, B * H), chunks / 4));
+    const int64_t per = (chunks + want - 1) / want;
+    *tokens = (int)(per * kC);
+    *segs = (int)((chunks + per - 1) / per);
+}
+
+}  // namespace
+
+bool la_tc_fits(int64_t T, int64_t Dk, int64_t Dv, int dtype) {
+    if ((dtype != CT_BF16 && dtype != CT_F16) || Dk > 128 || Dv > 128 || T <= kLaScanTokens) return false;
+    DeviceInfo d;
+    return device_info(&d) != cudaSuccess || (d.cc_major == 10 && d.cc_minor == 3);
+}
+
+bool la_tc_supports(const LaCore& c) {
+    return la_tc_fits(c.T, c.Da, c.Db, c.dtype) && c.B * c.H < (1ll << 24) && tma_ok(c, c.z, c.zs) && tma_ok(c, c.x, c.xs) &&
+           tma_ok(c, c.y, c.ys) && (!c.out || tma_ok(c, c.out, c.os));
+}
+
+size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
+    if (!la_tc_fits(T, Dk, Dv, dtype)) return 0;
+    DeviceInfo d;
+    int sm = 152, segs, tokens;
+    if (device_info(&d) == cudaSuccess) sm = d.sm_count;
+    split(B, T, H, sm, &segs, &tokens);
+    const size_t m = (size_t)B * H * Dk * Dv * sizeof(float);
+    return (segs > 1 ? round256(m * segs) : 0) + (dtype == CT_F16 ? round256(m) + round256((size_t)B * H * sizeof(int)) : 0);
+}
+
+cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t s) {
+    DeviceInfo d;
+    cudaError_t e = device_info(&d);
+    if (e != cudaSuccess) return e;
+    LaTcParams P;
+    std::memset(&P, 0, sizeof(P));
+    split(c.B, c.T, c.H, d.sm_count, &P.segs, &P.seg_tokens);
+    if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db) ||
+        (c.out && !map_tensor(&P.to, c, c.out, c.os, c.Db)))
+        return cudaErrorInvalidValue;
+    const int64_t BH = c.B * c.H, msize = (int64_t)c.Da * c.Db;
+    char* ws = static_cast<char*>(workspace);
+    float* sums = nullptr;
+    if (P.segs > 1) {
+        sums = reinterpret_cast<float*>(ws);
+        ws += round256((size_t)BH * msize * P.segs * sizeof(float));
+    }
+    // f16: results are kept aside until it is known that no value left the
+    // type's range (state_out may be state_in, which the second try reads)
+    float* m_out = c.m_out;
+    int* flags = nullptr;
+    if (c.dtype == CT_F16) {
+        if (c.m_out) m_out = reinterpret_cast<float*>(ws);
+        ws += round256((size_t)BH * msize * sizeof(float));
+        flags = reinterpret_cast<int*>(ws);
+        e = cudaMemsetAsync(flags, 0, (size_t)BH * sizeof(int), s);
+        if (e != cudaSuccess) return e;
+    }
+    P.out = c.out;
+    for (int i = 0; i < 3; ++i) P.os[i] = c.os[i];
+    P.log_decay = c.log_decay;
+    P.lengths = c.lengths;
+    P.flags = flags;
+    P.mscale = c.mscale;
+    P.oscale = c.oscale;
+    P.reverse = c.reverse;
+    P.T = c.T;
+    P.H = c.H;
+    P.Da = c.Da;
+    P.Db = c.Db;
+    P.BH = (int)BH;
+    P.wait_ns = wait_limit_ns();
+    const uint32_t type = c.dtype == CT_BF16 ? 1u : 0u;
+    const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(128 >> 4) << 24);  // D f32, M = 128
+    P.idesc_s = common | ((uint32_t)(kC >> 3) << 17);
+    P.idesc_n = common | (1u << 16) | ((uint32_t)((c.Db <= 64 ? 64 : 128) >> 3) << 17);
+    if (P.segs > 1) {
+        P.m_out = sums;
+        e = launch_t<true>(P, c.dtype, s);
+        if (e != cudaSuccess) return e;
+        la_chain<<<(unsigned)((BH * msize + 255) / 256), 256, 0, s>>>(sums, c.m_in, c.m_in_t, m_out, c.log_decay, c.lengths, c.reverse,
+                                                                     c.T, c.H, c.Da, c.Db, (int)BH, P.seg_tokens, P.segs);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        P.m_in = sums;
+        P.m_in_seg = 1;
+        P.m_out = nullptr;
+    } else {
+        P.m_in = c.m_in;
+        P.m_in_t = c.m_in_t;
+        P.m_out = m_out;
+        P.final = 1;
+    }
+    if (c.out) e = launch_t<false>(P, c.dtype, s);
+    else if (P.segs == 1) e = launch_t<true>(P, c.dtype, s);  // only the last matrix is asked for
+    if (e != cudaSuccess || !flags) return e;
+    return launch_la_scan(c, s, flags, m_out);
+}
+
+cudaError_t la_error_word(unsigned int* v, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(v, g_device_error, sizeof(*v));
+    if (e == cudaSuccess && clear && *v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace ct
