@@ -22,9 +22,15 @@
 // One CTA per sequence, head and segment walks its chunks in order:
 //   warps 0-7   S -> P, and out: TMEM row = token, two halves of the columns
 //   warps 8-11  decayed x (TMEM row = column of X), then the scaling of Z M
-//   warps 12-15 M: fp32 -> hi, lo in shared memory, times decay^e in TMEM
-//   warp 16     TMA loads; warp 17 MMA issue; warp 18 TMA stores
-// so that the tensor cores run one product while the others are prepared.
+//   warps 12-19 M: fp32 -> hi, lo in shared memory, times decay^e in TMEM
+//               (Da <= 64: half of these share the decayed x instead)
+//   warp 20     TMA loads; warp 23 TMA stores
+//   warps 21, 22 issue the MMAs of S and P Y, and of Z M and the new M
+// so that the tensor cores run one product while the others are prepared.  The
+// two chains (S -> P -> out and M -> M) meet in Z M only, and each has its own
+// issuing thread: one thread for both spent half of its time in the other
+// chain's waits.  Loops are kept rolled: unrolled, the roles' code together
+// outgrew the instruction cache and waited for it more than for anything else.
 // Bound by memory at full occupancy: 4 x 128 x D x 2 bytes a chunk (5650
 // cycles of the SM's share of the copy rate at D = 128) against 3600 cycles of
 // MMAs.
@@ -46,7 +52,7 @@ namespace {
 using namespace tcg;
 
 constexpr int kC = 128;            // tokens of a chunk
-constexpr int kLaThreads = 19 * 32;
+constexpr int kLaThreads = 24 * 32;
 constexpr uint32_t kTmemP = 0, kTmemX = 128, kTmemO = 256, kTmemM = 384;
 constexpr float kF16Max = 65504.f;
 
@@ -75,7 +81,6 @@ struct LaShape {
     static constexpr uint32_t kX = 256 * DA, kY = 256 * DB, kM = 2 * DA * DB;
     static constexpr uint32_t oZ = 0, oX = 2 * kZ, oY = oX + kX, oM = oY + 2 * kY;
     static constexpr uint32_t kBytes = oM + 2 * kM;
-    static constexpr size_t kSmem = kBytes + 1024;
 };
 
 // MN-major operand, 128-byte swizzle: rows of 64 MN elements per K index,
@@ -108,14 +113,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16 lanes x 16 columns: thread i holds lanes i / 4 and i / 4 + 8, columns
-// i % 4 of every four (the layout of a transposed ldmatrix of 16-bit pairs).
-__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// 16 lanes x 32 columns: thread i holds lanes i / 4 (even registers) and
+// i / 4 + 8 (odd ones), column i % 4 of every four: the layout of a transposed
+// ldmatrix of 16-bit pairs.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, transposed.
 __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t* r) {
@@ -160,12 +180,21 @@ template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
 template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// v = hi + lo to within U^2 |v|, each half a T.
+// v = hi + lo to within U^2 |v|, each half a T.  bf16 takes the upper half of
+// the fp32 word as it is (no conversion instruction); lo has the rest.
 template <typename T>
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack2<T>(a, b);
-    const float2 h = unpack2<T>(hi);
-    lo = pack2<T>(a - h.x, b - h.y);
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+    float2 h;
+    if constexpr (std::is_same<T, __half>::value) {
+        hi = pack2<T>(v.x, v.y);
+        h = unpack2<T>(hi);
+    } else {
+        const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+        hi = __byte_perm(a, b, 0x7632);
+        h = make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u));
+    }
+    const float2 r = __ffma2_rn(h, make_float2(-1.f, -1.f), v);
+    lo = pack2<T>(r.x, r.y);
 }
 
 template <typename T, int DA, int DB, bool STATE>
@@ -176,12 +205,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // parts' steps then are 2^-28 and 2^-30, the ranges 4094 and 1023; beyond
     // them the flag has the head done again
     constexpr float kUp = kHalf ? 16.f : 1.f, kUpX = kHalf ? 64.f : 1.f;
+    // warp groups of the decayed x and of M: three between them
+    constexpr int kXGroups = DA <= 64 ? 2 : 1, kMGroups = 3 - kXGroups;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t z_full[2], x_full, y_full[2], z_free[2], x_free, y_free[2];
-    __shared__ uint64_t s_ready, zm_ready, zm_done, p_done, x_done, m_done, o_ready, m_ready, o_free, staged, drain_bar;
+    __shared__ uint64_t s_ready, zm_ready, zm_done, p_done, x_done, m_done, o_ready, m_ready, o_free, staged, drain_bar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ float tab[2 * kC];   // tab[kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j
+    __shared__ __align__(8) float tab[2][2 * kC];   // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]: one later
     __shared__ float pw[kC + 2];    // decay^k
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -214,37 +245,46 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     }
 
     const float g = fmaxf(P.log_decay[h], -1e30f);
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    // the tiles' swizzle needs 1024-byte alignment, which the declaration asks
+    // for; there is no room to round up (227 KiB are used at 128 x 128)
+    const uint32_t base = smem_u32(smem_raw);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_device_error, kErrProducer);
+        return;
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&z_full[i]), 1);
             mbar_init(smem_u32(&y_full[i]), 1);
             mbar_init(smem_u32(&z_free[i]), 1);
-            mbar_init(smem_u32(&y_free[i]), 1);
+            mbar_init(smem_u32(&y_free[i]), STATE ? 1 : 2);
         }
         mbar_init(smem_u32(&x_full), 1);
-        mbar_init(smem_u32(&x_free), STATE ? 4 : 5);
+        mbar_init(smem_u32(&x_free), 4 * kXGroups + (STATE ? 0 : 1));
         mbar_init(smem_u32(&s_ready), 1);
         mbar_init(smem_u32(&zm_ready), 1);
         mbar_init(smem_u32(&zm_done), 4);
         mbar_init(smem_u32(&p_done), 8);
-        mbar_init(smem_u32(&x_done), 4);
-        mbar_init(smem_u32(&m_done), 4);
+        mbar_init(smem_u32(&x_done), 4 * kXGroups);
+        mbar_init(smem_u32(&m_done), 4 * kMGroups);
         mbar_init(smem_u32(&o_ready), 1);
         mbar_init(smem_u32(&m_ready), 1);
         mbar_init(smem_u32(&o_free), 8);
         mbar_init(smem_u32(&staged), 8);
-        mbar_init(smem_u32(&drain_bar), 1);
+        mbar_init(smem_u32(&drain_bar[0]), 1);
+        mbar_init(smem_u32(&drain_bar[1]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
     if (threadIdx.x < kC + 1) pw[threadIdx.x] = expf((float)threadIdx.x * g);
     for (int i = threadIdx.x; i < 2 * kC; i += kLaThreads) {
         const int d = P.reverse ? i - (kC - 1) : (kC - 1) - i;
-        tab[i] = d < 0 ? 0.f : expf((float)d * g) * (P.mscale * P.oscale * kUp);
+        const float f = d < 0 ? 0.f : expf((float)d * g) * (P.mscale * P.oscale * kUp);
+        tab[0][i] = f;
+        if (i > 0) tab[1][i - 1] = f;
     }
-    if (warp == 17) {
+    if (warp == 21) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -269,28 +309,36 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 const int n = rows_of(chunk_at(c));
                 if (!waits(s_ready, c, kErrEpilogue)) break;
                 tc_fence_after();
-                float v[2][32];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) tmem_ld32(lane_base + kTmemP + half * 64 + q * 32, v[q]);
-                tmem_ld_wait();
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 2; ++q) {
-                    const int j0 = half * 64 + q * 32;
-                    uint32_t hi[16], lo[16];
-                    const float* f = tab + (kC - 1) + j0 - row;
+                    const int cb = half * 2 + q, j0 = cb * 32, rb = warp & 3;
+                    uint32_t u[32];  // hi, then lo
+                    if (P.reverse ? cb < rb : cb > rb) {  // none of the 32 columns is seen by the 32 rows
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[q][i] *= f[i];
-                    if (n < kC)  // rows after the end hold anything, NaN included
+                        for (int i = 0; i < 32; ++i) u[i] = 0;
+                    } else {
+                        float v[32];
+                        tmem_ld32(lane_base + kTmemP + j0, v);
+                        tmem_ld_wait();
+                        const int at = (kC - 1) + j0 - row;
+                        const float2* f = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (row >= n || j0 + i >= n || (P.reverse ? j0 + i < row : j0 + i > row)) v[q][i] = 0.f;
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f[i]);
+                            v[2 * i] = m.x;
+                            v[2 * i + 1] = m.y;
+                        }
+                        if (n < kC)  // rows after the end hold anything, NaN included
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        split2<T>(v[q][2 * i], v[q][2 * i + 1], hi[i], lo[i]);
-                        if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[q][2 * i]), fabsf(v[q][2 * i + 1])));
+                            for (int i = 0; i < 32; ++i)
+                                if (row >= n || j0 + i >= n || (P.reverse ? j0 + i < row : j0 + i > row)) v[i] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            split2<T>(make_float2(v[2 * i], v[2 * i + 1]), u[i], u[16 + i]);
+                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+                        }
                     }
-                    tmem_st16(lane_base + kTmemP + j0, hi);
-                    tmem_st16(lane_base + kTmemP + j0 + 16, lo);
+                    tmem_st32(lane_base + kTmemP + j0, u);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -299,33 +347,33 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 if (!waits(o_ready, c, kErrEpilogue)) break;
                 tc_fence_after();
                 const uint32_t stage = base + Sh::oZ + (c & 1) * Sh::kZ;
-#pragma unroll
-                for (int q = 0; q < DB / 64; ++q) tmem_ld32(lane_base + kTmemO + half * (DB / 2) + q * 32, v[q]);
-                tmem_ld_wait();
-                tc_fence_before();
-                warp_arrive(o_free, lane);
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < DB / 64; ++q) {
                     const int col = half * (DB / 2) + q * 32;
+                    float v[32];
+                    tmem_ld32(lane_base + kTmemO + col, v);
+                    tmem_ld_wait();
                     const uint32_t at = stage + (col / 64) * 16384u + row * 128u;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t u[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            u[i] = row < n ? pack2<T>(v[q][8 * k + 2 * i] * (1.f / kUp), v[q][8 * k + 2 * i + 1] * (1.f / kUp)) : 0u;
+                            u[i] = row < n ? pack2<T>(v[8 * k + 2 * i] * (1.f / kUp), v[8 * k + 2 * i + 1] * (1.f / kUp)) : 0u;
                         sts128(at + ((((col & 63) >> 3) + k) ^ (row & 7)) * 16u, u[0], u[1], u[2], u[3]);
                     }
                 }
+                tc_fence_before();
+                warp_arrive(o_free, lane);
                 fence_async_smem();
                 warp_arrive(staged, lane);
             }
             if constexpr (kHalf)
                 if (!(top <= kF16Max)) P.flags[bh] = 1;
         }
-    } else if (warp < 12) {
+    } else if (warp < 12 || (kXGroups == 2 && warp >= 16 && warp < 20)) {
         // ------------------------------------- decayed x, scaling of Z M
-        const int w4 = warp & 3;
+        const int w4 = warp & 3, xg = warp >= 16 ? 1 : 0;
         const bool fed = w4 * 32 < DA;  // the others' rows no column of X feeds
         [[maybe_unused]] float top = 0.f;
         if (!fed) {
@@ -340,46 +388,59 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         // matrices (x columns 0-7 | 8-15) x (tokens 0-7), then tokens 8-15
         const uint32_t xs = base + Sh::oX + (uint32_t)(w4 >> 1) * 16384u + ((lane & 7) + (lane >> 4) * 8) * 128u;
         const uint32_t ch = (uint32_t)(w4 & 1) * 4 + ((lane >> 3) & 1);
+        const float xscale = P.mscale * kUpX;
         for (int c = 0; c < n_chunks; ++c) {
             const int n = rows_of(chunk_at(c));
             if (!waits(x_full, c, kErrEpilogue)) break;
             bool ok = true;
             if (fed) {
+                uint32_t x[8];  // 32 tokens x 16 columns of x
+                auto fetch = [&](int blk) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        ldsm4_trans(xs + ((blk >> 1) * 32 + 16 * k) * 128u + (((ch + (blk & 1) * 2) ^ (lane & 7)) << 4), x + 4 * k);
+                };
+                float2 f[4];
+                const int blk0 = xg * (8 / kXGroups), blk1 = blk0 + 8 / kXGroups;
+                fetch(blk0);
 #pragma unroll 1
-                for (int blk = 0; blk < 8 && ok; ++blk) {
-                    const int j0 = (blk >> 1) * 32, ah = blk & 1;  // 32 tokens x 16 columns of x
-                    uint32_t x[8], hi[8], lo[8];
+                for (int blk = blk0; blk < blk1; ++blk) {
+                    const int j0 = (blk >> 1) * 32 + 2 * (lane & 3);  // this lane's tokens: j0 + 8 m, + 1
+                    if ((blk & 1) == 0) {
+                        const float* at = P.reverse ? pw + j0 : pw + (n - 1 - j0);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) ldsm4_trans(xs + (j0 + 16 * k) * 128u + (((ch + ah * 2) ^ (lane & 7)) << 4), x + 4 * k);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {  // tokens j0 + 8 m + 2 (lane % 4), + 1
-                        const int j = j0 + 8 * m + 2 * (lane & 3);
-                        float f0 = pw[P.reverse ? j : max(n - 1 - j, 0)], f1 = pw[P.reverse ? j + 1 : max(n - 2 - j, 0)];
-                        f0 *= P.mscale * kUpX;
-                        f1 *= P.mscale * kUpX;
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float2 v = unpack2<T>(x[2 * m + r]);
-                            v.x = j < n ? v.x * f0 : 0.f;
-                            v.y = j + 1 < n ? v.y * f1 : 0.f;
-                            split2<T>(v.x, v.y, hi[2 * m + r], lo[2 * m + r]);
-                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        for (int m = 0; m < 4; ++m) {
+                            const int j = 8 * m;
+                            f[m].x = j0 + j < n ? at[P.reverse ? j : -j] : 0.f;
+                            f[m].y = j0 + j + 1 < n ? at[P.reverse ? j + 1 : -j - 1] : 0.f;
+                            f[m] = __fmul2_rn(f[m], make_float2(xscale, xscale));
                         }
                     }
+                    uint32_t u[16];  // hi, then lo
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {  // r % 2: 8 columns; r / 2: 8 tokens
+                        float2 v = __fmul2_rn(unpack2<T>(x[r]), f[r >> 1]);
+                        if (n < kC) {  // what lies after the end may be NaN
+                            if (j0 + 8 * (r >> 1) >= n) v.x = 0.f;
+                            if (j0 + 8 * (r >> 1) + 1 >= n) v.y = 0.f;
+                        }
+                        split2<T>(v, u[r], u[8 + r]);
+                        if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                    if (blk + 1 < blk1) fetch(blk + 1);
                     // the MMAs of the chunk before have read these places
-                    if (blk == 0 && c > 0) {
+                    if (blk == blk0 && c > 0) {
                         ok = waits(m_ready, c - 1, kErrEpilogue);
+                        if (!ok) break;
                         tc_fence_after();
                     }
-                    const uint32_t at = lane_base + ((uint32_t)(ah * 16) << 16) + kTmemX + j0;
-                    tmem_st_16x16(at, hi);
-                    tmem_st_16x16(at + 16, lo);
+                    tmem_st_16x32(lane_base + ((uint32_t)((blk & 1) * 16) << 16) + kTmemX + (blk >> 1) * 32, u);
                 }
                 tmem_st_wait();
             }
             if (!ok) break;
             warp_arrive(x_free, lane);
-            if (n < kC) {  // rows of Y after the end meet factors of 0: they must be finite
+            if (n < kC && xg == 0) {  // rows of Y after the end meet factors of 0: they must be finite
                 if (!waits(y_full[c & 1], c >> 1, kErrEpilogue)) break;
                 const uint32_t ys = base + Sh::oY + (c & 1) * Sh::kY;
                 for (int i = threadIdx.x - 256; i < (kC - n) * 8 * (DB / 64); i += 128) {
@@ -390,26 +451,25 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             }
             tc_fence_before();
             warp_arrive(x_done, lane);
-            if constexpr (!STATE) {
+            if (!STATE && xg == 0) {
                 if (!waits(zm_ready, c, kErrEpilogue)) break;
                 tc_fence_after();
                 const int row = w4 * 32 + lane, w = P.reverse ? n - row - (holds_end && c == 0 ? 1 : 0) : row + 1;
                 const float f = row < n ? pw[w] * P.oscale * kUp : 0.f;
 #pragma unroll 1
-                for (int q = 0; q < DB / 64; ++q) {
-                    const uint32_t at = lane_base + kTmemO + q * 64;
-                    float v[2][32];
-                    tmem_ld32(at, v[0]);
-                    tmem_ld32(at + 32, v[1]);
+                for (int q = 0; q < DB / 32; ++q) {
+                    const uint32_t at = lane_base + kTmemO + q * 32;
+                    float v[32];
+                    tmem_ld32(at, v);
                     tmem_ld_wait();
-                    uint32_t u[2][32];
+                    uint32_t u[32];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) u[k][i] = row < n ? __float_as_uint(v[k][i] * f) : 0u;
-                        tmem_st16(at + k * 32, u[k]);
-                        tmem_st16(at + k * 32 + 16, u[k] + 16);
+                    for (int i = 0; i < 16; ++i) {  // rows after the end may hold NaN; they are not stored
+                        const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
+                        u[2 * i] = __float_as_uint(m.x);
+                        u[2 * i + 1] = __float_as_uint(m.y);
                     }
+                    tmem_st32(at, u);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -418,9 +478,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         }
         if constexpr (kHalf)
             if (!(top <= kF16Max)) P.flags[bh] = 1;
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // -------------------------------------------------------------- M
-        const int a = (warp & 3) * 32 + lane;
+        const int a = (warp & 3) * 32 + lane, half = (warp - 12) >> 2;
         [[maybe_unused]] float top = 0.f;
         for (int c = 0; c <= n_chunks; ++c) {
             if (c > 0) {
@@ -431,51 +491,52 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             const float f = c < n_chunks ? pw[n - (holds_end && c == 0 ? 1 : 0)] * kUpX : 1.f;
             const float last = P.reverse && P.final ? pw[1] : 1.f;
 #pragma unroll 1
-            for (int q = 0; q < DB / 64; ++q) {
-                float v[64];
+            for (int q = 0; q < DB / 32 / kMGroups; ++q) {
+                const int col0 = half * (DB / 2) + q * 32;
+                float v[32];
                 if (c == 0) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const int col = q * 64 + i;
+                    for (int i = 0; i < 32; ++i) {
+                        const int col = col0 + i;
                         v[i] = 0.f;
                         if (m_in && a < P.Da && col < P.Db) v[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + a : (int64_t)a * P.Db + col];
                     }
                 } else {
-                    tmem_ld32(lane_base + kTmemM + q * 64, v);
-                    tmem_ld32(lane_base + kTmemM + q * 64 + 32, v + 32);
+                    tmem_ld32(lane_base + kTmemM + col0, v);
                     tmem_ld_wait();
                     if constexpr (kHalf)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) v[i] *= 1.f / kUpX;
+                        for (int i = 0; i < 32; ++i) v[i] *= 1.f / kUpX;
                 }
                 if (c == n_chunks) {
                     if (m_out && a < P.Da)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (q * 64 + i < P.Db) m_out[(int64_t)a * P.Db + q * 64 + i] = v[i] * last;
+                        for (int i = 0; i < 32; ++i)
+                            if (col0 + i < P.Db) m_out[(int64_t)a * P.Db + col0 + i] = v[i] * last;
                     continue;
                 }
-                if (!STATE && a < DA) {
-                    const uint32_t at = base + Sh::oM + (uint32_t)q * (DA * 128u) + (uint32_t)a * 128u;
+                uint32_t s[32];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                for (int i = 0; i < 16; ++i) {
+                    const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
+                    s[2 * i] = __float_as_uint(m.x);
+                    s[2 * i + 1] = __float_as_uint(m.y);
+                }
+                tmem_st32(lane_base + kTmemM + col0, s);
+                if (!STATE && a < DA) {
+                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)a * 128u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            split2<T>(v[8 * k + 2 * i], v[8 * k + 2 * i + 1], hi[i], lo[i]);
+                            split2<T>(make_float2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]), hi[i], lo[i]);
                             if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[8 * k + 2 * i]), fabsf(v[8 * k + 2 * i + 1])));
                         }
-                        const uint32_t o = ((uint32_t)k ^ (uint32_t)(a & 7)) * 16u;
+                        const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(a & 7)) * 16u;
                         sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
                         sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
                     }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t u[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[16 * k + i] * f);
-                    tmem_st16(lane_base + kTmemM + q * 64 + k * 16, u);
                 }
             }
             if (c == n_chunks) break;
@@ -486,7 +547,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         }
         if constexpr (kHalf)
             if (!(top <= kF16Max)) P.flags[bh] = 1;
-    } else if (warp == 16) {
+    } else if (warp == 20) {
         // ------------------------------------------------------- TMA loads
         if (lane == 0) {
             int nz = 0, ny = 0, nx = 0;  // fills issued
@@ -523,21 +584,32 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             }
         }
         __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp < 23) {
         // ------------------------------------------------------- MMA issue
+        const bool chain_p = warp == 21;
         if (lane == 0) {
             auto wait1 = [&](uint64_t& bar, int parity) {
                 return mbar_wait(smem_u32(&bar), (uint32_t)parity & 1u, kErrMma, &abort_flag, P.wait_ns);
             };
-            for (int c = 0; c < n_chunks; ++c) {
-                const int s = c & 1;
-                const uint32_t zs = base + Sh::oZ + s * Sh::kZ, xs = base + Sh::oX, ys = base + Sh::oY + s * Sh::kY;
-                if constexpr (!STATE) {
+            // D += A B over the chunk's tokens, A = hi + lo in TMEM
+            auto by_y = [&](uint32_t d, uint32_t at, int s) {
+                const uint64_t yd = desc_mn(base + Sh::oY + s * Sh::kY, 16384);
+#pragma unroll 4
+                for (int k = 0; k < kC / 16; ++k) {
+                    const uint32_t ad = at + (k / 2) * 32 + (k & 1) * 8;
+                    mma_ts(d, ad, yd + 128 * k, P.idesc_n, 1);
+                    mma_ts(d, ad + 16, yd + 128 * k, P.idesc_n, 1);
+                }
+            };
+            if (chain_p) {
+                for (int c = 0; c < n_chunks && !STATE; ++c) {
+                    const int s = c & 1;
+                    const uint32_t zs = base + Sh::oZ + s * Sh::kZ, xs = base + Sh::oX;
                     if (!wait1(z_full[s], c >> 1) || !wait1(x_full, c)) break;
                     // P of the chunk before has been multiplied: its place takes S
                     if (c > 0 && !wait1(o_ready, c - 1)) break;
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 4
                     for (int k = 0; k < DA / 16; ++k) {
                         const uint32_t o = (k / 4) * 16384u;
                         mma_f16(tmem + kTmemP, smem_desc_sw128(zs + o) + 2 * (k & 3), smem_desc_sw128(xs + o) + 2 * (k & 3), P.idesc_s,
@@ -545,46 +617,43 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     }
                     mma_commit(smem_u32(&s_ready));
                     mma_commit(smem_u32(&x_free));
-                    if (!wait1(m_done, c)) break;
-                    if (c > 0 && !wait1(o_free, c - 1)) break;
+                    // (zm_done also tells that Y's rows after the end are cleared)
+                    if (!wait1(y_full[s], c >> 1) || !wait1(zm_done, c) || !wait1(p_done, c)) break;
                     tc_fence_after();
-                    const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
-#pragma unroll
-                    for (int k = 0; k < DA / 16; ++k) {
-                        const uint64_t ad = smem_desc_sw128(zs + (k / 4) * 16384u) + 2 * (k & 3);
-                        mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
-                        mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
-                    }
-                    mma_commit(smem_u32(&zm_ready));
-                } else {
-                    if (!wait1(m_done, c)) break;
-                }
-                if (!wait1(x_done, c) || !wait1(y_full[s], c >> 1)) break;
-                tc_fence_after();
-                const uint64_t yd = desc_mn(ys, 16384);
-#pragma unroll
-                for (int k = 0; k < kC / 16; ++k) {
-                    const uint32_t xa = tmem + kTmemX + (k / 2) * 32 + (k & 1) * 8;
-                    mma_ts(tmem + kTmemM, xa, yd + 128 * k, P.idesc_n, 1);
-                    mma_ts(tmem + kTmemM, xa + 16, yd + 128 * k, P.idesc_n, 1);
-                }
-                mma_commit(smem_u32(&m_ready));
-                if constexpr (!STATE) {
-                    if (!wait1(zm_done, c) || !wait1(p_done, c)) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < kC / 16; ++k) {
-                        const uint32_t pa = tmem + kTmemP + (k / 2) * 32 + (k & 1) * 8;
-                        mma_ts(tmem + kTmemO, pa, yd + 128 * k, P.idesc_n, 1);
-                        mma_ts(tmem + kTmemO, pa + 16, yd + 128 * k, P.idesc_n, 1);
-                    }
+                    by_y(tmem + kTmemO, tmem + kTmemP, s);
                     mma_commit(smem_u32(&o_ready));
+                    mma_commit(smem_u32(&y_free[s]));
                 }
-                mma_commit(smem_u32(&y_free[s]));
+            } else {
+                for (int c = 0; c < n_chunks; ++c) {
+                    const int s = c & 1;
+                    if constexpr (!STATE) {
+                        if (!wait1(z_full[s], c >> 1)) break;
+                        if (c > 0 && !wait1(o_free, c - 1)) break;
+                        if (!wait1(m_done, c)) break;
+                        tc_fence_after();
+                        const uint32_t zs = base + Sh::oZ + s * Sh::kZ;
+                        const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
+#pragma unroll 4
+                        for (int k = 0; k < DA / 16; ++k) {
+                            const uint64_t ad = smem_desc_sw128(zs + (k / 4) * 16384u) + 2 * (k & 3);
+                            mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
+                            mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
+                        }
+                        mma_commit(smem_u32(&zm_ready));
+                    } else {
+                        if (!wait1(m_done, c)) break;
+                    }
+                    if (!wait1(y_full[s], c >> 1) || !wait1(x_done, c)) break;
+                    tc_fence_after();
+                    by_y(tmem + kTmemM, tmem + kTmemX, s);
+                    mma_commit(smem_u32(&m_ready));
+                    mma_commit(smem_u32(&y_free[s]));
+                }
             }
             // no MMA may be in flight when TMEM is released
-            mma_commit(smem_u32(&drain_bar));
-            mbar_drain(smem_u32(&drain_bar), 0);
+            mma_commit(smem_u32(&drain_bar[chain_p ? 0 : 1]));
+            mbar_drain(smem_u32(&drain_bar[chain_p ? 0 : 1]), 0);
         }
         __syncwarp();
     } else if (!STATE) {
@@ -606,7 +675,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 17)
+    if (warp == 21)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -659,7 +728,7 @@ bool tma_ok(const LaCore& c, const void* p, const int64_t (&st)[3]) {
 template <typename T, int DA, int DB, bool STATE>
 cudaError_t launch_k(const LaTcParams& P, cudaStream_t s) {
     auto k = la_chunks<T, DA, DB, STATE>;
-    constexpr int bytes = (int)LaShape<DA, DB>::kSmem;
+    constexpr int bytes = (int)LaShape<DA, DB>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)(P.BH * P.segs), kLaThreads, bytes, s>>>(P);
