@@ -5,8 +5,8 @@
 // With the chunk's rows Z, X (128 x Da), Y (128 x Db), a row i's distance
 // d(i, j) >= 0 to the rows it sees, and M the matrix before the chunk:
 //   S   = Z X^T                          128 x 128
-//   P   = S * decay^d(i,j) * mscale * oscale, 0 where j is not seen by i
-//   out = P Y + (oscale * decay^w(i)) * (Z M)
+//   P   = S * decay^d(i,j) * mscale, 0 where j is not seen by i
+//   out = oscale * (P Y + decay^w(i) * (Z M))
 //   M  <- decay^e M + (mscale * decay^f(j) x_j)^T Y
 // forward in time (n rows in the chunk): d = i - j, w = i + 1, f = n - 1 - j,
 // e = n; backward: d = j - i, w = n - i, f = j, e = n, one less in w and e for
@@ -19,18 +19,18 @@
 // out itself, and the fp32 state's 2^-9.  P and x enter from TMEM (P over S,
 // in place), M from shared memory.
 //
-// One CTA per sequence, head and segment walks its chunks in order:
-//   warps 0-7   S -> P, and out: TMEM row = token, two halves of the columns
-//   warps 8-11  decayed x (TMEM row = column of X), then the scaling of Z M
-//   warps 12-19 M: fp32 -> hi, lo in shared memory, times decay^e in TMEM
-//               (Da <= 64: half of these share the decayed x instead)
-//   warp 20     TMA loads; warp 23 TMA stores
-//   warps 21, 22 issue the MMAs of S and P Y, and of Z M and the new M
-// so that the tensor cores run one product while the others are prepared.  The
-// two chains (S -> P -> out and M -> M) meet in Z M only, and each has its own
-// issuing thread: one thread for both spent half of its time in the other
-// chain's waits.  Loops are kept rolled: unrolled, the roles' code together
-// outgrew the instruction cache and waited for it more than for anything else.
+// One CTA per sequence, head and segment walks its chunks in order.  Sixteen
+// warps do the same step of the work at the same time, each a lane quarter of
+// TMEM and a quarter of the columns (or tokens):
+//   A  M: fp32 -> hi, lo in shared memory, times decay^e in TMEM; decayed x
+//   B  out of the chunk before: TMEM -> memory;  S -> P
+//   C  the scaling of Z M
+// while the tensor cores run P Y of the chunk before and S under A, and the
+// new M and Z M under B.  Warps with a role each (P, x, M at the same time) came
+// first: their bodies evicted one another from the instruction caches and a
+// warp issued once in 13 cycles (8 x 2048 x 16 heads of 128: 93 us).
+// One more warp loads tiles by TMA into a ring of five that Z, X and Y take in
+// turn, one issues the MMAs.
 // Bound by memory at full occupancy: 4 x 128 x D x 2 bytes a chunk (5650
 // cycles of the SM's share of the copy rate at D = 128) against 3600 cycles of
 // MMAs.
@@ -52,14 +52,16 @@ namespace {
 using namespace tcg;
 
 constexpr int kC = 128;            // tokens of a chunk
-constexpr int kLaThreads = 24 * 32;
+constexpr int kLaWorkers = 16;     // warps
+constexpr int kLaThreads = (kLaWorkers + 2) * 32;
 constexpr uint32_t kTmemP = 0, kTmemX = 128, kTmemO = 256, kTmemM = 384;
 constexpr float kF16Max = 65504.f;
 
 struct LaTcParams {
-    CUtensorMap tz, tx, ty, to;  // (D, T, H, B), boxes of 64 columns x 128 tokens
+    CUtensorMap tz, tx, ty;      // (D, T, H, B), boxes of 64 columns x 128 tokens
     void* out;
     int64_t os[3];
+    int out_vec;                 // out's rows take stores of 16 bytes (1) or 32 (2)
     const float* m_in;           // before segment 0 of the walk, or per segment
     int m_in_t, m_in_seg;        // transposed; one for each segment ([seg][bh][Da][Db])
     float* m_out;                // after the walk of a segment ([seg][bh])
@@ -74,13 +76,15 @@ struct LaTcParams {
     uint64_t wait_ns;
 };
 
+// Tile n of the walk (Z, X, Y of chunk 0, Z, X, Y of chunk 1, ...) lies in
+// place n % 5 of the ring; M's hi and lo parts after it.
 template <int DA, int DB>
 struct LaShape {
-    static constexpr int kD = DA > DB ? DA : DB;
-    static constexpr uint32_t kZ = 256 * kD;     // also out's staging
-    static constexpr uint32_t kX = 256 * DA, kY = 256 * DB, kM = 2 * DA * DB;
-    static constexpr uint32_t oZ = 0, oX = 2 * kZ, oY = oX + kX, oM = oY + 2 * kY;
-    static constexpr uint32_t kBytes = oM + 2 * kM;
+    static constexpr uint32_t kTile = 256 * (DA > DB ? DA : DB), kM = 2 * DA * DB;
+    static constexpr uint32_t oM = 5 * kTile, kBytes = oM + 2 * kM;
+    static __device__ __forceinline__ uint32_t z(int c) { return (uint32_t)(3 * c % 5) * kTile; }
+    static __device__ __forceinline__ uint32_t x(int c) { return (uint32_t)((3 * c + 1) % 5) * kTile; }
+    static __device__ __forceinline__ uint32_t y(int c) { return (uint32_t)((3 * c + 2) % 5) * kTile; }
 };
 
 // MN-major operand, 128-byte swizzle: rows of 64 MN elements per K index,
@@ -150,12 +154,25 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane) {
     if (lane == 0) mbar_arrive(smem_u32(&bar));
 }
 
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float* v) {
+    if constexpr (N == 32) tmem_ld32(taddr, v);
+    else tmem_ld16(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t* r) {
+    if constexpr (N == 32) tmem_st32(taddr, r);
+    else tmem_st16(taddr, r);
+}
+// Adjacent values times f.
+template <int N>
+__device__ __forceinline__ void scaled(const float* v, float f, uint32_t* u) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
+        u[2 * i] = __float_as_uint(m.x);
+        u[2 * i + 1] = __float_as_uint(m.y);
+    }
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -197,6 +214,32 @@ __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
     lo = pack2<T>(r.x, r.y);
 }
 
+// N columns of a row (32 or 16), packed two to a word, of which `left` exist.
+// A thread has a row, so its bytes are consecutive; stores of 32 bytes write
+// whole sectors.
+template <typename T, int N>
+__device__ __forceinline__ void store_cols(T* to, const uint32_t* u, int left, int vec) {
+    if (vec == 2 && left >= N) {
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * k), "r"(u[8 * k]), "r"(u[8 * k + 1]),
+                         "r"(u[8 * k + 2]), "r"(u[8 * k + 3]), "r"(u[8 * k + 4]), "r"(u[8 * k + 5]), "r"(u[8 * k + 6]), "r"(u[8 * k + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < N / 8; ++k) {
+            if (vec && left >= 8 * k + 8) {
+                *reinterpret_cast<uint4*>(to + 8 * k) = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (8 * k + i < left)
+                        reinterpret_cast<unsigned short*>(to)[8 * k + i] = (unsigned short)(u[4 * k + i / 2] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
 template <typename T, int DA, int DB, bool STATE>
 __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcParams P) {
     using Sh = LaShape<DA, DB>;
@@ -205,11 +248,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // parts' steps then are 2^-28 and 2^-30, the ranges 4094 and 1023; beyond
     // them the flag has the head done again
     constexpr float kUp = kHalf ? 16.f : 1.f, kUpX = kHalf ? 64.f : 1.f;
-    // warp groups of the decayed x and of M: three between them
-    constexpr int kXGroups = DA <= 64 ? 2 : 1, kMGroups = 3 - kXGroups;
+    constexpr int kN = DB / 4;  // columns of Y, M and out a warp has
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t z_full[2], x_full, y_full[2], z_free[2], x_free, y_free[2];
-    __shared__ uint64_t s_ready, zm_ready, zm_done, p_done, x_done, m_done, o_ready, m_ready, o_free, staged, drain_bar[2];
+    __shared__ uint64_t z_full[2], x_full[2], y_full[2], z_free[2], x_free[2], y_free[2];
+    __shared__ uint64_t s_ready, zm_ready, a_done, p_done, o_ready, m_ready, o_free, drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     __shared__ __align__(8) float tab[2][2 * kC];   // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]: one later
@@ -257,34 +299,30 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&z_full[i]), 1);
             mbar_init(smem_u32(&y_full[i]), 1);
+            mbar_init(smem_u32(&y_free[i]), 1);
             mbar_init(smem_u32(&z_free[i]), 1);
-            mbar_init(smem_u32(&y_free[i]), STATE ? 1 : 2);
+            mbar_init(smem_u32(&x_full[i]), 1);
+            mbar_init(smem_u32(&x_free[i]), kLaWorkers + (STATE ? 0 : 1));
         }
-        mbar_init(smem_u32(&x_full), 1);
-        mbar_init(smem_u32(&x_free), 4 * kXGroups + (STATE ? 0 : 1));
         mbar_init(smem_u32(&s_ready), 1);
         mbar_init(smem_u32(&zm_ready), 1);
-        mbar_init(smem_u32(&zm_done), 4);
-        mbar_init(smem_u32(&p_done), 8);
-        mbar_init(smem_u32(&x_done), 4 * kXGroups);
-        mbar_init(smem_u32(&m_done), 4 * kMGroups);
+        mbar_init(smem_u32(&a_done), kLaWorkers);
+        mbar_init(smem_u32(&p_done), kLaWorkers);
         mbar_init(smem_u32(&o_ready), 1);
         mbar_init(smem_u32(&m_ready), 1);
-        mbar_init(smem_u32(&o_free), 8);
-        mbar_init(smem_u32(&staged), 8);
-        mbar_init(smem_u32(&drain_bar[0]), 1);
-        mbar_init(smem_u32(&drain_bar[1]), 1);
+        mbar_init(smem_u32(&o_free), kLaWorkers);
+        mbar_init(smem_u32(&drain_bar), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
     if (threadIdx.x < kC + 1) pw[threadIdx.x] = expf((float)threadIdx.x * g);
     for (int i = threadIdx.x; i < 2 * kC; i += kLaThreads) {
         const int d = P.reverse ? i - (kC - 1) : (kC - 1) - i;
-        const float f = d < 0 ? 0.f : expf((float)d * g) * (P.mscale * P.oscale * kUp);
+        const float f = d < 0 ? 0.f : expf((float)d * g) * (P.mscale * kUp);
         tab[0][i] = f;
         if (i > 0) tab[1][i - 1] = f;
     }
-    if (warp == 21) {
+    if (warp == kLaWorkers + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -300,27 +338,165 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)parity & 1u, code, &abort_flag, P.wait_ns));
     };
 
-    if (warp < 8) {
-        // ----------------------------------------------------------- P, out
-        if constexpr (!STATE) {
-            const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-            [[maybe_unused]] float top = 0.f;
-            for (int c = 0; c < n_chunks; ++c) {
-                const int n = rows_of(chunk_at(c));
-                if (!waits(s_ready, c, kErrEpilogue)) break;
+    if (warp < kLaWorkers) {
+        const int w4 = warp & 3, g4 = warp >> 2;
+        const int row = w4 * 32 + lane, col0 = g4 * kN;
+        const bool fed = w4 * 32 < DA;  // columns of X feed this lane quarter of the decayed x and of M
+        [[maybe_unused]] float top = 0.f;
+        bool ok = true;
+        if (!fed) {
+            uint32_t zero[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) zero[i] = 0;
+            tmem_st32(lane_base + kTmemX + g4 * 32, zero);
+            tmem_stn<kN>(lane_base + kTmemM + col0, zero);
+            tmem_st_wait();
+        }
+        // ldmatrix: lanes 0-7, 8-15, 16-23, 24-31 point at the rows of the
+        // matrices (x columns 0-7 | 8-15) x (tokens 0-7), then tokens 8-15
+        const uint32_t xs = base + (uint32_t)(w4 >> 1) * 16384u + (g4 * 32 + (lane & 7) + (lane >> 4) * 8) * 128u;
+        const uint32_t ch = (uint32_t)(w4 & 1) * 4 + ((lane >> 3) & 1);
+        const int j0 = g4 * 32 + 2 * (lane & 3);  // this lane's tokens of x: j0 + 8 m, + 1
+
+        auto write_out = [&](int c) {  // waits for out of chunk c, false where that gave up
+            const int n = rows_of(chunk_at(c));
+            if (!waits(o_ready, c, kErrEpilogue)) return false;
+            tc_fence_after();
+            float v[kN];
+            tmem_ldn<kN>(lane_base + kTmemO + col0, v);
+            tmem_ld_wait();
+            tc_fence_before();
+            warp_arrive(o_free, lane);
+            const int t = s0 + chunk_at(c) * kC + row;
+            const float2 os = make_float2(P.oscale / kUp, P.oscale / kUp);
+            uint32_t u[kN / 2];
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) {
+                const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), os);
+                u[i] = row < n ? pack2<T>(m.x, m.y) : 0u;
+            }
+            if (t < P.T)
+                store_cols<T, kN>(static_cast<T*>(P.out) + b * P.os[0] + (int64_t)t * P.os[1] + h * P.os[2] + col0, u, P.Db - col0,
+                                  P.out_vec);
+            return true;
+        };
+
+        for (int c = 0; c < n_chunks; ++c) {
+            const int n = rows_of(chunk_at(c));
+            const int first = holds_end && c == 0 ? 1 : 0;
+            // ------------------------------------------------------- A: M
+            if (c > 0) {
+                ok = waits(m_ready, c - 1, kErrEpilogue);
+                if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    const int cb = half * 2 + q, j0 = cb * 32, rb = warp & 3;
-                    uint32_t u[32];  // hi, then lo
-                    if (P.reverse ? cb < rb : cb > rb) {  // none of the 32 columns is seen by the 32 rows
+            }
+            if (fed) {
+                float v[kN];
+                if (c == 0) {
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {
+                        const int col = col0 + i;
+                        v[i] = 0.f;
+                        if (m_in && row < P.Da && col < P.Db)
+                            v[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + row : (int64_t)row * P.Db + col];
+                    }
+                } else {
+                    tmem_ldn<kN>(lane_base + kTmemM + col0, v);
+                    tmem_ld_wait();
+                    if constexpr (kHalf)
+#pragma unroll
+                        for (int i = 0; i < kN; ++i) v[i] *= 1.f / kUpX;
+                }
+                uint32_t u[kN];
+                scaled<kN>(v, pw[n - first] * kUpX, u);
+                tmem_stn<kN>(lane_base + kTmemM + col0, u);
+                if constexpr (!STATE) {
+                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)row * 128u;
+#pragma unroll
+                    for (int k = 0; k < kN / 8; ++k) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 m = make_float2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+                            split2<T>(m, hi[i], lo[i]);
+                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(m.x), fabsf(m.y)));
+                        }
+                        const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(row & 7)) * 16u;
+                        sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
+                        sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+            }
+            // ----------------------------------------------- A: decayed x
+            ok = waits(x_full[c & 1], c >> 1, kErrEpilogue);
+            if (!ok) break;
+            if (fed) {
+                // the factors of the last row forward in time (0 for tokens
+                // after it), of the first one backward
+                const int at = (P.reverse ? kC - 1 : kC - n) + j0;
+                const float2* ft = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
+                float2 f[4];
+                uint32_t x[2][8];  // 32 tokens x 16 columns of x
+#pragma unroll
+                for (int ah = 0; ah < 2; ++ah)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        ldsm4_trans(xs + Sh::x(c) + k * 2048u + (((ch + ah * 2) ^ (lane & 7)) << 4), x[ah] + 4 * k);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    f[m] = ft[4 * m];
+                    if constexpr (kUpX != kUp) f[m] = __fmul2_rn(f[m], make_float2(kUpX / kUp, kUpX / kUp));
+                }
+#pragma unroll
+                for (int ah = 0; ah < 2; ++ah) {
+                    uint32_t u[16];  // hi, then lo
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {  // r % 2: 8 columns; r / 2: 8 tokens
+                        float2 v = __fmul2_rn(unpack2<T>(x[ah][r]), f[r >> 1]);
+                        if (n < kC) {  // what lies after the end may be NaN
+                            if (j0 + 8 * (r >> 1) >= n) v.x = 0.f;
+                            if (j0 + 8 * (r >> 1) + 1 >= n) v.y = 0.f;
+                        }
+                        split2<T>(v, u[r], u[8 + r]);
+                        if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                    tmem_st_16x32(lane_base + ((uint32_t)(ah * 16) << 16) + kTmemX + g4 * 32, u);
+                }
+                tmem_st_wait();
+            }
+            warp_arrive(x_free[c & 1], lane);
+            if (n < kC) {  // rows of Y after the end meet factors of 0: they must be finite
+                ok = waits(y_full[c & 1], c >> 1, kErrEpilogue);
+                if (!ok) break;
+                const uint32_t ys = base + Sh::y(c);
+                for (int i = threadIdx.x; i < (kC - n) * 8 * (DB / 64); i += kLaWorkers * 32) {
+                    const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
+                    sts128(ys + blk * 16384u + (uint32_t)(n + r / 8) * 128u + (uint32_t)(r % 8) * 16u, 0, 0, 0, 0);
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            warp_arrive(a_done, lane);
+            if constexpr (!STATE) {
+                // ---------------------------------------------- B: out, P
+                if (c > 0) {
+                    ok = write_out(c - 1);
+                    if (!ok) break;
+                }
+                ok = waits(s_ready, c, kErrEpilogue);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const int p0 = g4 * 32;  // columns of S
+                    uint32_t u[32];          // hi, then lo
+                    if (P.reverse ? g4 < w4 : g4 > w4) {  // none of the 32 columns is seen by the 32 rows
 #pragma unroll
                         for (int i = 0; i < 32; ++i) u[i] = 0;
                     } else {
                         float v[32];
-                        tmem_ld32(lane_base + kTmemP + j0, v);
+                        tmem_ld32(lane_base + kTmemP + p0, v);
                         tmem_ld_wait();
-                        const int at = (kC - 1) + j0 - row;
+                        const int at = (kC - 1) + p0 - row;
                         const float2* f = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -331,269 +507,96 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                         if (n < kC)  // rows after the end hold anything, NaN included
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (row >= n || j0 + i >= n || (P.reverse ? j0 + i < row : j0 + i > row)) v[i] = 0.f;
+                                if (row >= n || p0 + i >= n || (P.reverse ? p0 + i < row : p0 + i > row)) v[i] = 0.f;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             split2<T>(make_float2(v[2 * i], v[2 * i + 1]), u[i], u[16 + i]);
                             if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
                         }
                     }
-                    tmem_st32(lane_base + kTmemP + j0, u);
+                    tmem_st32(lane_base + kTmemP + p0, u);
                 }
-                tmem_st_wait();
+                // --------------------------------------------- C: Z M
+                ok = waits(zm_ready, c, kErrEpilogue);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const int w = P.reverse ? n - row - first : row + 1;
+                    float v[kN];
+                    uint32_t u[kN];
+                    tmem_ldn<kN>(lane_base + kTmemO + col0, v);
+                    tmem_ld_wait();
+                    // rows after the end may hold NaN; they are not stored
+                    scaled<kN>(v, row < n ? pw[w] * kUp : 0.f, u);
+                    tmem_stn<kN>(lane_base + kTmemO + col0, u);
+                    tmem_st_wait();
+                }
                 tc_fence_before();
                 warp_arrive(p_done, lane);
-
-                if (!waits(o_ready, c, kErrEpilogue)) break;
-                tc_fence_after();
-                const uint32_t stage = base + Sh::oZ + (c & 1) * Sh::kZ;
-#pragma unroll 1
-                for (int q = 0; q < DB / 64; ++q) {
-                    const int col = half * (DB / 2) + q * 32;
-                    float v[32];
-                    tmem_ld32(lane_base + kTmemO + col, v);
-                    tmem_ld_wait();
-                    const uint32_t at = stage + (col / 64) * 16384u + row * 128u;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            u[i] = row < n ? pack2<T>(v[8 * k + 2 * i] * (1.f / kUp), v[8 * k + 2 * i + 1] * (1.f / kUp)) : 0u;
-                        sts128(at + ((((col & 63) >> 3) + k) ^ (row & 7)) * 16u, u[0], u[1], u[2], u[3]);
-                    }
-                }
-                tc_fence_before();
-                warp_arrive(o_free, lane);
-                fence_async_smem();
-                warp_arrive(staged, lane);
             }
-            if constexpr (kHalf)
-                if (!(top <= kF16Max)) P.flags[bh] = 1;
         }
-    } else if (warp < 12 || (kXGroups == 2 && warp >= 16 && warp < 20)) {
-        // ------------------------------------- decayed x, scaling of Z M
-        const int w4 = warp & 3, xg = warp >= 16 ? 1 : 0;
-        const bool fed = w4 * 32 < DA;  // the others' rows no column of X feeds
-        [[maybe_unused]] float top = 0.f;
-        if (!fed) {
-            uint32_t zero[16];
+        if (ok && waits(m_ready, n_chunks - 1, kErrEpilogue)) {
+            tc_fence_after();
+            if (m_out && fed) {
+                float v[kN];
+                tmem_ldn<kN>(lane_base + kTmemM + col0, v);
+                tmem_ld_wait();
+                const float last = (P.reverse && P.final ? pw[1] : 1.f) / kUpX;
+                if (row < P.Da)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) zero[i] = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tmem_st16(lane_base + kTmemX + i * 16, zero);
-            tmem_st_wait();
-        }
-        // ldmatrix: lanes 0-7, 8-15, 16-23, 24-31 point at the rows of the
-        // matrices (x columns 0-7 | 8-15) x (tokens 0-7), then tokens 8-15
-        const uint32_t xs = base + Sh::oX + (uint32_t)(w4 >> 1) * 16384u + ((lane & 7) + (lane >> 4) * 8) * 128u;
-        const uint32_t ch = (uint32_t)(w4 & 1) * 4 + ((lane >> 3) & 1);
-        const float xscale = P.mscale * kUpX;
-        for (int c = 0; c < n_chunks; ++c) {
-            const int n = rows_of(chunk_at(c));
-            if (!waits(x_full, c, kErrEpilogue)) break;
-            bool ok = true;
-            if (fed) {
-                uint32_t x[8];  // 32 tokens x 16 columns of x
-                auto fetch = [&](int blk) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        ldsm4_trans(xs + ((blk >> 1) * 32 + 16 * k) * 128u + (((ch + (blk & 1) * 2) ^ (lane & 7)) << 4), x + 4 * k);
-                };
-                float2 f[4];
-                const int blk0 = xg * (8 / kXGroups), blk1 = blk0 + 8 / kXGroups;
-                fetch(blk0);
-#pragma unroll 1
-                for (int blk = blk0; blk < blk1; ++blk) {
-                    const int j0 = (blk >> 1) * 32 + 2 * (lane & 3);  // this lane's tokens: j0 + 8 m, + 1
-                    if ((blk & 1) == 0) {
-                        const float* at = P.reverse ? pw + j0 : pw + (n - 1 - j0);
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const int j = 8 * m;
-                            f[m].x = j0 + j < n ? at[P.reverse ? j : -j] : 0.f;
-                            f[m].y = j0 + j + 1 < n ? at[P.reverse ? j + 1 : -j - 1] : 0.f;
-                            f[m] = __fmul2_rn(f[m], make_float2(xscale, xscale));
-                        }
-                    }
-                    uint32_t u[16];  // hi, then lo
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {  // r % 2: 8 columns; r / 2: 8 tokens
-                        float2 v = __fmul2_rn(unpack2<T>(x[r]), f[r >> 1]);
-                        if (n < kC) {  // what lies after the end may be NaN
-                            if (j0 + 8 * (r >> 1) >= n) v.x = 0.f;
-                            if (j0 + 8 * (r >> 1) + 1 >= n) v.y = 0.f;
-                        }
-                        split2<T>(v, u[r], u[8 + r]);
-                        if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                    }
-                    if (blk + 1 < blk1) fetch(blk + 1);
-                    // the MMAs of the chunk before have read these places
-                    if (blk == blk0 && c > 0) {
-                        ok = waits(m_ready, c - 1, kErrEpilogue);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    tmem_st_16x32(lane_base + ((uint32_t)((blk & 1) * 16) << 16) + kTmemX + (blk >> 1) * 32, u);
-                }
-                tmem_st_wait();
+                    for (int i = 0; i < kN; ++i)
+                        if (col0 + i < P.Db) m_out[(int64_t)row * P.Db + col0 + i] = v[i] * last;
             }
-            if (!ok) break;
-            warp_arrive(x_free, lane);
-            if (n < kC && xg == 0) {  // rows of Y after the end meet factors of 0: they must be finite
-                if (!waits(y_full[c & 1], c >> 1, kErrEpilogue)) break;
-                const uint32_t ys = base + Sh::oY + (c & 1) * Sh::kY;
-                for (int i = threadIdx.x - 256; i < (kC - n) * 8 * (DB / 64); i += 128) {
-                    const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
-                    sts128(ys + blk * 16384u + (uint32_t)(n + r / 8) * 128u + (uint32_t)(r % 8) * 16u, 0, 0, 0, 0);
-                }
-                fence_async_smem();
-            }
-            tc_fence_before();
-            warp_arrive(x_done, lane);
-            if (!STATE && xg == 0) {
-                if (!waits(zm_ready, c, kErrEpilogue)) break;
-                tc_fence_after();
-                const int row = w4 * 32 + lane, w = P.reverse ? n - row - (holds_end && c == 0 ? 1 : 0) : row + 1;
-                const float f = row < n ? pw[w] * P.oscale * kUp : 0.f;
-#pragma unroll 1
-                for (int q = 0; q < DB / 32; ++q) {
-                    const uint32_t at = lane_base + kTmemO + q * 32;
-                    float v[32];
-                    tmem_ld32(at, v);
-                    tmem_ld_wait();
-                    uint32_t u[32];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {  // rows after the end may hold NaN; they are not stored
-                        const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
-                        u[2 * i] = __float_as_uint(m.x);
-                        u[2 * i + 1] = __float_as_uint(m.y);
-                    }
-                    tmem_st32(at, u);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                warp_arrive(zm_done, lane);
-            }
+            if constexpr (!STATE) write_out(n_chunks - 1);
         }
         if constexpr (kHalf)
             if (!(top <= kF16Max)) P.flags[bh] = 1;
-    } else if (warp < 20) {
-        // -------------------------------------------------------------- M
-        const int a = (warp & 3) * 32 + lane, half = (warp - 12) >> 2;
-        [[maybe_unused]] float top = 0.f;
-        for (int c = 0; c <= n_chunks; ++c) {
-            if (c > 0) {
-                if (!waits(m_ready, c - 1, kErrEpilogue)) break;
-                tc_fence_after();
-            }
-            const int n = c < n_chunks ? rows_of(chunk_at(c)) : 0;
-            const float f = c < n_chunks ? pw[n - (holds_end && c == 0 ? 1 : 0)] * kUpX : 1.f;
-            const float last = P.reverse && P.final ? pw[1] : 1.f;
-#pragma unroll 1
-            for (int q = 0; q < DB / 32 / kMGroups; ++q) {
-                const int col0 = half * (DB / 2) + q * 32;
-                float v[32];
-                if (c == 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int col = col0 + i;
-                        v[i] = 0.f;
-                        if (m_in && a < P.Da && col < P.Db) v[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + a : (int64_t)a * P.Db + col];
-                    }
-                } else {
-                    tmem_ld32(lane_base + kTmemM + col0, v);
-                    tmem_ld_wait();
-                    if constexpr (kHalf)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= 1.f / kUpX;
-                }
-                if (c == n_chunks) {
-                    if (m_out && a < P.Da)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (col0 + i < P.Db) m_out[(int64_t)a * P.Db + col0 + i] = v[i] * last;
-                    continue;
-                }
-                uint32_t s[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
-                    s[2 * i] = __float_as_uint(m.x);
-                    s[2 * i + 1] = __float_as_uint(m.y);
-                }
-                tmem_st32(lane_base + kTmemM + col0, s);
-                if (!STATE && a < DA) {
-                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)a * 128u;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            split2<T>(make_float2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]), hi[i], lo[i]);
-                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[8 * k + 2 * i]), fabsf(v[8 * k + 2 * i + 1])));
-                        }
-                        const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(a & 7)) * 16u;
-                        sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
-                        sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
-                    }
-                }
-            }
-            if (c == n_chunks) break;
-            tmem_st_wait();
-            if (!STATE) fence_async_smem();
-            tc_fence_before();
-            warp_arrive(m_done, lane);
-        }
-        if constexpr (kHalf)
-            if (!(top <= kF16Max)) P.flags[bh] = 1;
-    } else if (warp == 20) {
+    } else if (warp == kLaWorkers) {
         // ------------------------------------------------------- TMA loads
         if (lane == 0) {
-            int nz = 0, ny = 0, nx = 0;  // fills issued
+            int nz = 0, nx = 0, ny = 0;  // fills issued
             bool ok = true;
+            auto fill = [&](const CUtensorMap* map, uint64_t& full, uint32_t place, int D, int t0) {
+                mbar_expect_tx(smem_u32(&full), 256 * D);
+                for (int k = 0; k < D / 64; ++k) tma_load_4d(base + place + k * 16384u, map, smem_u32(&full), k * 64, t0, h, b);
+            };
+            // a place was last used by the tile five before: X of two chunks
+            // ago for Z, Y of two chunks ago for X, the last chunk's Z for Y
             for (int c = 0; c < n_chunks; ++c) {
                 const int t0 = s0 + chunk_at(c) * kC, s = c & 1;
+                ok = c < 2 || mbar_wait(smem_u32(&x_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
+                if (!ok) break;
                 if (!STATE) {
-                    ok = c < 2 || mbar_wait(smem_u32(&z_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
-                    if (!ok) break;
-                    mbar_expect_tx(smem_u32(&z_full[s]), 256 * DA);
-                    for (int k = 0; k < DA / 64; ++k)
-                        tma_load_4d(base + Sh::oZ + s * Sh::kZ + k * 16384u, &P.tz, smem_u32(&z_full[s]), k * 64, t0, h, b);
+                    fill(&P.tz, z_full[s], Sh::z(c), DA, t0);
                     ++nz;
                 }
                 ok = c < 2 || mbar_wait(smem_u32(&y_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
                 if (!ok) break;
-                mbar_expect_tx(smem_u32(&y_full[s]), 256 * DB);
-                for (int k = 0; k < DB / 64; ++k)
-                    tma_load_4d(base + Sh::oY + s * Sh::kY + k * 16384u, &P.ty, smem_u32(&y_full[s]), k * 64, t0, h, b);
-                ++ny;
-                ok = c < 1 || mbar_wait(smem_u32(&x_free), (c - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
-                if (!ok) break;
-                mbar_expect_tx(smem_u32(&x_full), 256 * DA);
-                for (int k = 0; k < DA / 64; ++k)
-                    tma_load_4d(base + Sh::oX + k * 16384u, &P.tx, smem_u32(&x_full), k * 64, t0, h, b);
+                fill(&P.tx, x_full[s], Sh::x(c), DA, t0);
                 ++nx;
+                ok = STATE || c < 1 || mbar_wait(smem_u32(&z_free[s ^ 1]), ((c - 1) >> 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
+                if (!ok) break;
+                fill(&P.ty, y_full[s], Sh::y(c), DB, t0);
+                ++ny;
             }
             if (!ok) {
                 // what was issued must land before the CTA exits: the last
-                // fill of each slot
+                // fill of each barrier
                 for (int i = max(0, nz - 2); i < nz; ++i) mbar_drain(smem_u32(&z_full[i & 1]), (i >> 1) & 1);
+                for (int i = max(0, nx - 2); i < nx; ++i) mbar_drain(smem_u32(&x_full[i & 1]), (i >> 1) & 1);
                 for (int i = max(0, ny - 2); i < ny; ++i) mbar_drain(smem_u32(&y_full[i & 1]), (i >> 1) & 1);
-                if (nx > 0) mbar_drain(smem_u32(&x_full), (nx - 1) & 1);
             }
         }
         __syncwarp();
-    } else if (warp < 23) {
+    } else {
         // ------------------------------------------------------- MMA issue
-        const bool chain_p = warp == 21;
         if (lane == 0) {
             auto wait1 = [&](uint64_t& bar, int parity) {
                 return mbar_wait(smem_u32(&bar), (uint32_t)parity & 1u, kErrMma, &abort_flag, P.wait_ns);
             };
             // D += A B over the chunk's tokens, A = hi + lo in TMEM
-            auto by_y = [&](uint32_t d, uint32_t at, int s) {
-                const uint64_t yd = desc_mn(base + Sh::oY + s * Sh::kY, 16384);
+            auto by_y = [&](uint32_t d, uint32_t at, int c) {
+                const uint64_t yd = desc_mn(base + Sh::y(c), 16384);
 #pragma unroll 4
                 for (int k = 0; k < kC / 16; ++k) {
                     const uint32_t ad = at + (k / 2) * 32 + (k & 1) * 8;
@@ -601,11 +604,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     mma_ts(d, ad + 16, yd + 128 * k, P.idesc_n, 1);
                 }
             };
-            if (chain_p) {
-                for (int c = 0; c < n_chunks && !STATE; ++c) {
-                    const int s = c & 1;
-                    const uint32_t zs = base + Sh::oZ + s * Sh::kZ, xs = base + Sh::oX;
-                    if (!wait1(z_full[s], c >> 1) || !wait1(x_full, c)) break;
+            for (int c = 0; c < n_chunks; ++c) {
+                const int s = c & 1;
+                if constexpr (!STATE) {
+                    const uint32_t zs = base + Sh::z(c), xs = base + Sh::x(c);
+                    if (!wait1(z_full[s], c >> 1) || !wait1(x_full[s], c >> 1)) break;
                     // P of the chunk before has been multiplied: its place takes S
                     if (c > 0 && !wait1(o_ready, c - 1)) break;
                     tc_fence_after();
@@ -616,58 +619,39 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                                 k > 0);
                     }
                     mma_commit(smem_u32(&s_ready));
-                    mma_commit(smem_u32(&x_free));
-                    // (zm_done also tells that Y's rows after the end are cleared)
-                    if (!wait1(y_full[s], c >> 1) || !wait1(zm_done, c) || !wait1(p_done, c)) break;
-                    tc_fence_after();
-                    by_y(tmem + kTmemO, tmem + kTmemP, s);
-                    mma_commit(smem_u32(&o_ready));
-                    mma_commit(smem_u32(&y_free[s]));
+                    mma_commit(smem_u32(&x_free[s]));
                 }
-            } else {
-                for (int c = 0; c < n_chunks; ++c) {
-                    const int s = c & 1;
-                    if constexpr (!STATE) {
-                        if (!wait1(z_full[s], c >> 1)) break;
-                        if (c > 0 && !wait1(o_free, c - 1)) break;
-                        if (!wait1(m_done, c)) break;
-                        tc_fence_after();
-                        const uint32_t zs = base + Sh::oZ + s * Sh::kZ;
-                        const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
+                if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
+                tc_fence_after();
+                by_y(tmem + kTmemM, tmem + kTmemX, c);
+                if constexpr (!STATE) {
+                    if (c > 0 && !wait1(o_free, c - 1)) break;
+                    tc_fence_after();
+                    const uint32_t zs = base + Sh::z(c);
+                    const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
 #pragma unroll 4
-                        for (int k = 0; k < DA / 16; ++k) {
-                            const uint64_t ad = smem_desc_sw128(zs + (k / 4) * 16384u) + 2 * (k & 3);
-                            mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
-                            mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
-                        }
-                        mma_commit(smem_u32(&zm_ready));
-                    } else {
-                        if (!wait1(m_done, c)) break;
+                    for (int k = 0; k < DA / 16; ++k) {
+                        const uint64_t ad = smem_desc_sw128(zs + (k / 4) * 16384u) + 2 * (k & 3);
+                        mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
+                        mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
                     }
-                    if (!wait1(y_full[s], c >> 1) || !wait1(x_done, c)) break;
-                    tc_fence_after();
-                    by_y(tmem + kTmemM, tmem + kTmemX, s);
+                    mma_commit(smem_u32(&zm_ready));
+                    mma_commit(smem_u32(&z_free[s]));
+                    // (M's shared copy has been read too by then: step A of the
+                    // next chunk writes it)
                     mma_commit(smem_u32(&m_ready));
-                    mma_commit(smem_u32(&y_free[s]));
+                    if (!wait1(p_done, c)) break;
+                    tc_fence_after();
+                    by_y(tmem + kTmemO, tmem + kTmemP, c);
+                    mma_commit(smem_u32(&o_ready));
+                } else {
+                    mma_commit(smem_u32(&m_ready));
                 }
+                mma_commit(smem_u32(&y_free[s]));
             }
             // no MMA may be in flight when TMEM is released
-            mma_commit(smem_u32(&drain_bar[chain_p ? 0 : 1]));
-            mbar_drain(smem_u32(&drain_bar[chain_p ? 0 : 1]), 0);
-        }
-        __syncwarp();
-    } else if (!STATE) {
-        // ------------------------------------------------------ TMA stores
-        if (lane == 0) {
-            for (int c = 0; c < n_chunks; ++c) {
-                if (!mbar_wait(smem_u32(&staged), c & 1, kErrEpilogue, &abort_flag, P.wait_ns)) break;
-                const int t0 = s0 + chunk_at(c) * kC;
-                for (int k = 0; k < DB / 64; ++k)
-                    if (k * 64 < P.Db) tma_store_4d(&P.to, base + Sh::oZ + (c & 1) * Sh::kZ + k * 16384u, k * 64, t0, h, b);
-                bulk_wait_read_all();
-                mbar_arrive(smem_u32(&z_free[c & 1]));
-            }
-            bulk_wait_all();
+            mma_commit(smem_u32(&drain_bar));
+            mbar_drain(smem_u32(&drain_bar), 0);
         }
         __syncwarp();
     }
@@ -675,7 +659,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 21)
+    if (warp == kLaWorkers + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -716,7 +700,7 @@ bool map_tensor(CUtensorMap* m, const LaCore& c, const void* p, const int64_t (&
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether TMA can read (or write) the tensor where it is.
+// Whether TMA can read the tensor where it is.
 bool tma_ok(const LaCore& c, const void* p, const int64_t (&st)[3]) {
     const int64_t n[3] = {c.B, c.T, c.H};
     if ((uintptr_t)p % 16 != 0) return false;
@@ -767,7 +751,7 @@ bool la_tc_fits(int64_t T, int64_t Dk, int64_t Dv, int dtype) {
 
 bool la_tc_supports(const LaCore& c) {
     return la_tc_fits(c.T, c.Da, c.Db, c.dtype) && c.B * c.H < (1ll << 24) && tma_ok(c, c.z, c.zs) && tma_ok(c, c.x, c.xs) &&
-           tma_ok(c, c.y, c.ys) && (!c.out || tma_ok(c, c.out, c.os));
+           tma_ok(c, c.y, c.ys);
 }
 
 size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
@@ -787,8 +771,7 @@ cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t s) {
     LaTcParams P;
     std::memset(&P, 0, sizeof(P));
     split(c.B, c.T, c.H, d.sm_count, &P.segs, &P.seg_tokens);
-    if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db) ||
-        (c.out && !map_tensor(&P.to, c, c.out, c.os, c.Db)))
+    if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db))
         return cudaErrorInvalidValue;
     const int64_t BH = c.B * c.H, msize = (int64_t)c.Da * c.Db;
     char* ws = static_cast<char*>(workspace);
@@ -810,6 +793,13 @@ cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t s) {
     }
     P.out = c.out;
     for (int i = 0; i < 3; ++i) P.os[i] = c.os[i];
+    auto rows_on = [&](int bytes) {
+        const int64_t n[3] = {c.B, c.T, c.H};
+        bool ok = (uintptr_t)c.out % bytes == 0;
+        for (int i = 0; i < 3; ++i) ok = ok && (n[i] <= 1 || c.os[i] % (bytes / 2) == 0);
+        return ok;
+    };
+    P.out_vec = rows_on(32) ? 2 : rows_on(16) ? 1 : 0;
     P.log_decay = c.log_decay;
     P.lengths = c.lengths;
     P.flags = flags;
