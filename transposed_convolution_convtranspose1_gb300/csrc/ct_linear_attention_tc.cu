@@ -22,15 +22,17 @@
 // One CTA per sequence, head and segment walks its chunks in order.  Sixteen
 // warps do the same step of the work at the same time, each a lane quarter of
 // TMEM and a quarter of the columns (or tokens):
-//   A  M: fp32 -> hi, lo in shared memory, times decay^e in TMEM; decayed x
+//   A  M times decay^e in TMEM, decayed x; then M's hi, lo to shared memory
 //   B  out of the chunk before: TMEM -> memory;  S -> P
 //   C  the scaling of Z M
-// while the tensor cores run P Y of the chunk before and S under A, and the
-// new M and Z M under B.  Warps with a role each (P, x, M at the same time) came
-// first: their bodies evicted one another from the instruction caches and a
-// warp issued once in 13 cycles (8 x 2048 x 16 heads of 128: 93 us).
+// while the tensor cores run P Y of the chunk before and S under A, the new M
+// under M's split, Z M under B.  Warps with a role each (P, x, M at the same
+// time) came first: their bodies evicted one another from the instruction
+// caches and a warp issued once in 13 cycles (8 x 2048 x 16 heads of 128:
+// 93 us).
 // One more warp loads tiles by TMA into a ring of five that Z, X and Y take in
-// turn, one issues the MMAs.
+// turn (X's place, once x is in TMEM, stages out for its TMA store), one issues
+// the MMAs.
 // Bound by memory at full occupancy: 4 x 128 x D x 2 bytes a chunk (5650
 // cycles of the SM's share of the copy rate at D = 128) against 3600 cycles of
 // MMAs.
@@ -59,9 +61,9 @@ constexpr float kF16Max = 65504.f;
 
 struct LaTcParams {
     CUtensorMap tz, tx, ty;      // (D, T, H, B), boxes of 64 columns x 128 tokens
+    CUtensorMap to;              // boxes of DB / 4 columns x 32 tokens
     void* out;
     int64_t os[3];
-    int out_vec;                 // out's rows take stores of 16 bytes (1) or 32 (2)
     const float* m_in;           // before segment 0 of the walk, or per segment
     int m_in_t, m_in_seg;        // transposed; one for each segment ([seg][bh][Da][Db])
     float* m_out;                // after the walk of a segment ([seg][bh])
@@ -214,30 +216,12 @@ __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
     lo = pack2<T>(r.x, r.y);
 }
 
-// N columns of a row (32 or 16), packed two to a word, of which `left` exist.
-// A thread has a row, so its bytes are consecutive; stores of 32 bytes write
-// whole sectors.
-template <typename T, int N>
-__device__ __forceinline__ void store_cols(T* to, const uint32_t* u, int left, int vec) {
-    if (vec == 2 && left >= N) {
-#pragma unroll
-        for (int k = 0; k < N / 16; ++k)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * k), "r"(u[8 * k]), "r"(u[8 * k + 1]),
-                         "r"(u[8 * k + 2]), "r"(u[8 * k + 3]), "r"(u[8 * k + 4]), "r"(u[8 * k + 5]), "r"(u[8 * k + 6]), "r"(u[8 * k + 7])
-                         : "memory");
-    } else {
-#pragma unroll
-        for (int k = 0; k < N / 8; ++k) {
-            if (vec && left >= 8 * k + 8) {
-                *reinterpret_cast<uint4*>(to + 8 * k) = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * k + i < left)
-                        reinterpret_cast<unsigned short*>(to)[8 * k + i] = (unsigned short)(u[4 * k + i / 2] >> (16 * (i & 1)));
-            }
-        }
-    }
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 template <typename T, int DA, int DB, bool STATE>
@@ -251,7 +235,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     constexpr int kN = DB / 4;  // columns of Y, M and out a warp has
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t z_full[2], x_full[2], y_full[2], z_free[2], x_free[2], y_free[2];
-    __shared__ uint64_t s_ready, zm_ready, a_done, p_done, o_ready, m_ready, o_free, drain_bar;
+    __shared__ uint64_t s_ready, m_ready, a_done, m_done, p_done, o_ready, o_free, drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     __shared__ __align__(8) float tab[2][2 * kC];   // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]: one later
@@ -305,8 +289,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             mbar_init(smem_u32(&x_free[i]), kLaWorkers + (STATE ? 0 : 1));
         }
         mbar_init(smem_u32(&s_ready), 1);
-        mbar_init(smem_u32(&zm_ready), 1);
         mbar_init(smem_u32(&a_done), kLaWorkers);
+        mbar_init(smem_u32(&m_done), kLaWorkers);
         mbar_init(smem_u32(&p_done), kLaWorkers);
         mbar_init(smem_u32(&o_ready), 1);
         mbar_init(smem_u32(&m_ready), 1);
@@ -358,74 +342,65 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         const uint32_t ch = (uint32_t)(w4 & 1) * 4 + ((lane >> 3) & 1);
         const int j0 = g4 * 32 + 2 * (lane & 3);  // this lane's tokens of x: j0 + 8 m, + 1
 
-        auto write_out = [&](int c) {  // waits for out of chunk c, false where that gave up
+        // out of chunk c (P Y is done), staged in the place of a tile that
+        // nothing reads any more, this warp's 32 rows x kN columns of it
+        auto write_out = [&](int c, uint32_t place) {
             const int n = rows_of(chunk_at(c));
-            if (!waits(o_ready, c, kErrEpilogue)) return false;
-            tc_fence_after();
             float v[kN];
             tmem_ldn<kN>(lane_base + kTmemO + col0, v);
             tmem_ld_wait();
             tc_fence_before();
             warp_arrive(o_free, lane);
-            const int t = s0 + chunk_at(c) * kC + row;
             const float2 os = make_float2(P.oscale / kUp, P.oscale / kUp);
-            uint32_t u[kN / 2];
+            const uint32_t tile = base + place + (uint32_t)warp * (32 * kN * 2);
+            // rows of 64 (32) bytes, swizzled as the tensor map says
+            const uint32_t at = tile + lane * (kN * 2), sw = kN == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
 #pragma unroll
-            for (int i = 0; i < kN / 2; ++i) {
-                const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), os);
-                u[i] = row < n ? pack2<T>(m.x, m.y) : 0u;
+            for (int k = 0; k < kN / 8; ++k) {
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 m = __fmul2_rn(make_float2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]), os);
+                    u[i] = row < n ? pack2<T>(m.x, m.y) : 0u;
+                }
+                sts128(at + (k ^ sw) * 16u, u[0], u[1], u[2], u[3]);
             }
-            if (t < P.T)
-                store_cols<T, kN>(static_cast<T*>(P.out) + b * P.os[0] + (int64_t)t * P.os[1] + h * P.os[2] + col0, u, P.Db - col0,
-                                  P.out_vec);
-            return true;
+            fence_async_smem();
+            __syncwarp();
+            const int t = s0 + chunk_at(c) * kC + w4 * 32;
+            if (lane == 0 && t < P.T && col0 < P.Db) tma_store_4d(&P.to, tile, col0, t, h, b);
         };
 
         for (int c = 0; c < n_chunks; ++c) {
             const int n = rows_of(chunk_at(c));
             const int first = holds_end && c == 0 ? 1 : 0;
             // ------------------------------------------------------- A: M
-            if (c > 0) {
+            // (what is needed of the chunk before was waited for in its step C)
+            if (STATE && c > 0) {
                 ok = waits(m_ready, c - 1, kErrEpilogue);
                 if (!ok) break;
                 tc_fence_after();
             }
+            float mv[kN];
             if (fed) {
-                float v[kN];
                 if (c == 0) {
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
                         const int col = col0 + i;
-                        v[i] = 0.f;
+                        mv[i] = 0.f;
                         if (m_in && row < P.Da && col < P.Db)
-                            v[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + row : (int64_t)row * P.Db + col];
+                            mv[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + row : (int64_t)row * P.Db + col];
                     }
                 } else {
-                    tmem_ldn<kN>(lane_base + kTmemM + col0, v);
+                    tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
                     tmem_ld_wait();
                     if constexpr (kHalf)
 #pragma unroll
-                        for (int i = 0; i < kN; ++i) v[i] *= 1.f / kUpX;
+                        for (int i = 0; i < kN; ++i) mv[i] *= 1.f / kUpX;
                 }
                 uint32_t u[kN];
-                scaled<kN>(v, pw[n - first] * kUpX, u);
+                scaled<kN>(mv, pw[n - first] * kUpX, u);
                 tmem_stn<kN>(lane_base + kTmemM + col0, u);
-                if constexpr (!STATE) {
-                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)row * 128u;
-#pragma unroll
-                    for (int k = 0; k < kN / 8; ++k) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 m = make_float2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
-                            split2<T>(m, hi[i], lo[i]);
-                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(m.x), fabsf(m.y)));
-                        }
-                        const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(row & 7)) * 16u;
-                        sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
-                        sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
-                    }
-                }
             }
             // ----------------------------------------------- A: decayed x
             ok = waits(x_full[c & 1], c >> 1, kErrEpilogue);
@@ -464,7 +439,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 }
                 tmem_st_wait();
             }
-            warp_arrive(x_free[c & 1], lane);
+            if (STATE) warp_arrive(x_free[c & 1], lane);
             if (n < kC) {  // rows of Y after the end meet factors of 0: they must be finite
                 ok = waits(y_full[c & 1], c >> 1, kErrEpilogue);
                 if (!ok) break;
@@ -473,19 +448,37 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
                     sts128(ys + blk * 16384u + (uint32_t)(n + r / 8) * 128u + (uint32_t)(r % 8) * 16u, 0, 0, 0, 0);
                 }
+                fence_async_smem();
             }
-            fence_async_smem();
             tc_fence_before();
             warp_arrive(a_done, lane);
             if constexpr (!STATE) {
-                // ---------------------------------------------- B: out, P
-                if (c > 0) {
-                    ok = write_out(c - 1);
-                    if (!ok) break;
+                // ------------------------------------------- A: M's parts
+                if (fed) {
+                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)row * 128u;
+#pragma unroll
+                    for (int k = 0; k < kN / 8; ++k) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 m = make_float2(mv[8 * k + 2 * i], mv[8 * k + 2 * i + 1]);
+                            split2<T>(m, hi[i], lo[i]);
+                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(m.x), fabsf(m.y)));
+                        }
+                        const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(row & 7)) * 16u;
+                        sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
+                        sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    fence_async_smem();
                 }
-                ok = waits(s_ready, c, kErrEpilogue);
+                warp_arrive(m_done, lane);
+                // ---------------------------------------------- B: out, P
+                // S is issued when P Y of the chunk before is done; it and
+                // every warp's step A have read X
+                ok = waits(s_ready, c, kErrEpilogue) && waits(a_done, c, kErrEpilogue);
                 if (!ok) break;
                 tc_fence_after();
+                if (c > 0) write_out(c - 1, Sh::x(c));
                 {
                     const int p0 = g4 * 32;  // columns of S
                     uint32_t u[32];          // hi, then lo
@@ -517,7 +510,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     tmem_st32(lane_base + kTmemP + p0, u);
                 }
                 // --------------------------------------------- C: Z M
-                ok = waits(zm_ready, c, kErrEpilogue);
+                ok = waits(m_ready, c, kErrEpilogue);
                 if (!ok) break;
                 tc_fence_after();
                 {
@@ -533,6 +526,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 }
                 tc_fence_before();
                 warp_arrive(p_done, lane);
+                if (lane == 0) {
+                    bulk_wait_read_all();  // X's place is free when out has left it
+                    mbar_arrive(smem_u32(&x_free[c & 1]));
+                }
+                __syncwarp();
             }
         }
         if (ok && waits(m_ready, n_chunks - 1, kErrEpilogue)) {
@@ -547,8 +545,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     for (int i = 0; i < kN; ++i)
                         if (col0 + i < P.Db) m_out[(int64_t)row * P.Db + col0 + i] = v[i] * last;
             }
-            if constexpr (!STATE) write_out(n_chunks - 1);
+            if constexpr (!STATE)
+                if (waits(o_ready, n_chunks - 1, kErrEpilogue)) {
+                    tc_fence_after();
+                    write_out(n_chunks - 1, Sh::x(n_chunks - 1));
+                }
         }
+        if (!STATE && lane == 0) bulk_wait_all();
+        __syncwarp();
         if constexpr (kHalf)
             if (!(top <= kF16Max)) P.flags[bh] = 1;
     } else if (warp == kLaWorkers) {
@@ -625,6 +629,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 tc_fence_after();
                 by_y(tmem + kTmemM, tmem + kTmemX, c);
                 if constexpr (!STATE) {
+                    if (!wait1(m_done, c)) break;
                     if (c > 0 && !wait1(o_free, c - 1)) break;
                     tc_fence_after();
                     const uint32_t zs = base + Sh::z(c);
@@ -635,11 +640,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                         mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
                         mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
                     }
-                    mma_commit(smem_u32(&zm_ready));
                     mma_commit(smem_u32(&z_free[s]));
-                    // (M's shared copy has been read too by then: step A of the
-                    // next chunk writes it)
-                    mma_commit(smem_u32(&m_ready));
+                    mma_commit(smem_u32(&m_ready));  // the new M and Z M
                     if (!wait1(p_done, c)) break;
                     tc_fence_after();
                     by_y(tmem + kTmemO, tmem + kTmemP, c);
@@ -687,20 +689,23 @@ __global__ void __launch_bounds__(256) la_chain(float* sums, const float* m_in, 
     if (m_out) m_out[i] = reverse && len > 0 ? expf(g) * cur : cur;
 }
 
-bool map_tensor(CUtensorMap* m, const LaCore& c, const void* p, const int64_t (&st)[3], int D) {
+bool map_tensor(CUtensorMap* m, const LaCore& c, const void* p, const int64_t (&st)[3], int D, int cols = 64, int rows = kC) {
     auto enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)c.T, (cuuint64_t)c.H, (cuuint64_t)c.B};
     // an axis of one element may have any stride
     const cuuint64_t strides[3] = {c.T > 1 ? (cuuint64_t)st[1] * 2 : 256, c.H > 1 ? (cuuint64_t)st[2] * 2 : 256,
                                    c.B > 1 ? (cuuint64_t)st[0] * 2 : 256};
-    const cuuint32_t box[4] = {64, (cuuint32_t)kC, 1, 1}, es[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)cols, (cuuint32_t)rows, 1, 1}, es[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle swizzle = cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                    : CU_TENSOR_MAP_SWIZZLE_32B;
     return enc(m, c.dtype == CT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-               const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether TMA can read the tensor where it is.
+// Whether TMA can read (or write) the tensor where it is.
 bool tma_ok(const LaCore& c, const void* p, const int64_t (&st)[3]) {
     const int64_t n[3] = {c.B, c.T, c.H};
     if ((uintptr_t)p % 16 != 0) return false;
@@ -751,7 +756,7 @@ bool la_tc_fits(int64_t T, int64_t Dk, int64_t Dv, int dtype) {
 
 bool la_tc_supports(const LaCore& c) {
     return la_tc_fits(c.T, c.Da, c.Db, c.dtype) && c.B * c.H < (1ll << 24) && tma_ok(c, c.z, c.zs) && tma_ok(c, c.x, c.xs) &&
-           tma_ok(c, c.y, c.ys);
+           tma_ok(c, c.y, c.ys) && (!c.out || tma_ok(c, c.out, c.os));
 }
 
 size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
@@ -771,7 +776,8 @@ cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t s) {
     LaTcParams P;
     std::memset(&P, 0, sizeof(P));
     split(c.B, c.T, c.H, d.sm_count, &P.segs, &P.seg_tokens);
-    if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db))
+    if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db) ||
+        (c.out && !map_tensor(&P.to, c, c.out, c.os, c.Db, c.Db <= 64 ? 16 : 32, 32)))
         return cudaErrorInvalidValue;
     const int64_t BH = c.B * c.H, msize = (int64_t)c.Da * c.Db;
     char* ws = static_cast<char*>(workspace);
@@ -793,13 +799,6 @@ cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t s) {
     }
     P.out = c.out;
     for (int i = 0; i < 3; ++i) P.os[i] = c.os[i];
-    auto rows_on = [&](int bytes) {
-        const int64_t n[3] = {c.B, c.T, c.H};
-        bool ok = (uintptr_t)c.out % bytes == 0;
-        for (int i = 0; i < 3; ++i) ok = ok && (n[i] <= 1 || c.os[i] % (bytes / 2) == 0);
-        return ok;
-    };
-    P.out_vec = rows_on(32) ? 2 : rows_on(16) ? 1 : 0;
     P.log_decay = c.log_decay;
     P.lengths = c.lengths;
     P.flags = flags;
