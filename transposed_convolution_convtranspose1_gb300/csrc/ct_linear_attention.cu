@@ -200,7 +200,7 @@ struct Workspace {
 };
 
 cudaError_t launch_core(const LaCore& c, void* workspace, cudaStream_t s) {
-    return la_tc_supports(c) ? launch_la_tc(c, workspace, s) : launch_la_scan(c, s);
+    return la_tc_supports(c) ? launch_la_tc(&c, 1, workspace, s) : launch_la_scan(c, s);
 }
 
 LaCore core_of(const float* log_decay, const int32_t* lengths, int64_t B, int64_t T, int64_t H, int dtype) {
@@ -226,8 +226,7 @@ extern "C" int ct_linear_attention_workspace_bytes(int64_t B, int64_t T, int64_t
     if (!bytes) return report_error(CT_ERR_NULL, "bytes is NULL");
     int rc = check(B, T, H, Dk, Dv, dtype);
     if (rc != CT_OK) return rc;
-    // the gradients use it one after the other
-    *bytes = la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype);
+    *bytes = la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, backward);
     return CT_OK;
 }
 
@@ -254,7 +253,7 @@ extern "C" int ct_linear_attention_forward(const void* q, const int64_t* q_strid
     c.oscale = scale;
     cudaStream_t s = (cudaStream_t)stream;
     Workspace ws;
-    rc = ws.take(workspace, workspace_bytes, la_tc_supports(c) ? la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype) : 0, s);
+    rc = ws.take(workspace, workspace_bytes, la_tc_supports(c) ? la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, 0) : 0, s);
     if (rc != CT_OK) return rc;
     return done(ws.give_back(launch_core(c, ws.p, s), s), "linear attention");
 }
@@ -280,31 +279,31 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         return report_error(CT_ERR_ALIGN, "pointers must be aligned to their element size");
     cudaStream_t s = (cudaStream_t)stream;
     Workspace ws;
-    rc = ws.take(workspace, workspace_bytes, la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype), s);
+    rc = ws.take(workspace, workspace_bytes, la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, 1), s);
     if (rc != CT_OK) return rc;
-    cudaError_t e = cudaSuccess;
+    // dstate_in may be dstate_out's own buffer: the walk that writes it is the
+    // last to read it
+    LaCore walks[3];
+    int n = 0;
     if (dq && T > 0) {
-        LaCore c = core_of(log_decay, lengths, B, T, H, dtype);
+        LaCore& c = walks[n++] = core_of(log_decay, lengths, B, T, H, dtype);
         c.x = v; c.y = k; c.z = dout; c.out = dq;
         set3(c.xs, v_strides); set3(c.ys, k_strides); set3(c.zs, do_strides); set3(c.os, dq_strides);
         c.Da = (int)Dv; c.Db = (int)Dk;
         c.m_in = state_in; c.m_in_t = 1;
         c.oscale = scale;
-        e = launch_core(c, ws.p, s);
     }
-    if (e == cudaSuccess && dk && T > 0) {
-        LaCore c = core_of(log_decay, lengths, B, T, H, dtype);
+    if (dk && T > 0) {
+        LaCore& c = walks[n++] = core_of(log_decay, lengths, B, T, H, dtype);
         c.x = dout; c.y = q; c.z = v; c.out = dk;
         set3(c.xs, do_strides); set3(c.ys, q_strides); set3(c.zs, v_strides); set3(c.os, dk_strides);
         c.Da = (int)Dv; c.Db = (int)Dk;
         c.m_in = dstate_out; c.m_in_t = 1;
         c.mscale = scale;
         c.reverse = 1;
-        e = launch_core(c, ws.p, s);
     }
-    // last, because dstate_in may be dstate_out's own buffer
-    if (e == cudaSuccess && ((dv && T > 0) || dstate_in)) {
-        LaCore c = core_of(log_decay, lengths, B, T, H, dtype);
+    if ((dv && T > 0) || dstate_in) {
+        LaCore& c = walks[n++] = core_of(log_decay, lengths, B, T, H, dtype);
         c.x = q; c.y = dout; c.z = k; c.out = T > 0 ? dv : nullptr;
         set3(c.xs, q_strides); set3(c.ys, do_strides); set3(c.zs, k_strides);
         if (dv) set3(c.os, dv_strides);
@@ -312,7 +311,14 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         c.m_in = dstate_out; c.m_out = dstate_in;
         c.mscale = scale;
         c.reverse = 1;
-        e = launch_core(c, ws.p, s);
     }
+    // together where their tiles are alike: three times the CTAs.  In one
+    // launch nothing orders the walks, so a shared buffer keeps them apart.
+    bool together = n > 1 && (dstate_in == nullptr || dstate_in != dstate_out) && (Dk <= 64) == (Dv <= 64);
+    for (int i = 0; i < n; ++i) together = together && walks[i].out && la_tc_supports(walks[i]);
+    cudaError_t e = cudaSuccess;
+    if (together) e = launch_la_tc(walks, n, ws.p, s);
+    else
+        for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_core(walks[i], ws.p, s);
     return done(ws.give_back(e, s), "linear attention backward");
 }

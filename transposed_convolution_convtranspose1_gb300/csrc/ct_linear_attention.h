@@ -51,8 +51,10 @@ cudaError_t launch_la_scan(const LaCore& c, cudaStream_t stream, const int* only
 // head sizes up to 128, tensors that TMA can address.
 bool la_tc_fits(int64_t T, int64_t Dk, int64_t Dv, int dtype);
 bool la_tc_supports(const LaCore& c);
-size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype);
-cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t stream);
+size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype, int backward);
+// Up to three walks at once, of one (Da, Db) up to the tiles' 64 or 128 and
+// one Da * Db, each with an output or none with one.
+cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream_t stream);
 cudaError_t la_error_word(unsigned int* v, bool clear);
 
 }  // namespace ct

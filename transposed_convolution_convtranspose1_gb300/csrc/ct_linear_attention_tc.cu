@@ -78,6 +78,12 @@ struct LaTcParams {
     uint64_t wait_ns;
 };
 
+// Up to three walks of one launch (the gradients of q, k and v).
+struct LaTcBatch {
+    LaTcParams core[3];
+    int ctas;                    // of one core
+};
+
 // Tile n of the walk (Z, X, Y of chunk 0, Z, X, Y of chunk 1, ...) lies in
 // place n % 5 of the ring; M's hi and lo parts after it.
 template <int DA, int DB>
@@ -166,14 +172,19 @@ __device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t* r) {
     if constexpr (N == 32) tmem_st32(taddr, r);
     else tmem_st16(taddr, r);
 }
-// Adjacent values times f.
+// N columns of TMEM <- v * f, 16 at a time (fewer registers at once).
 template <int N>
-__device__ __forceinline__ void scaled(const float* v, float f, uint32_t* u) {
+__device__ __forceinline__ void tmem_st_scaled(uint32_t taddr, const float* v, float f) {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
-        u[2 * i] = __float_as_uint(m.x);
-        u[2 * i + 1] = __float_as_uint(m.y);
+    for (int k = 0; k < N / 16; ++k) {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 m = __fmul2_rn(make_float2(v[16 * k + 2 * i], v[16 * k + 2 * i + 1]), make_float2(f, f));
+            u[2 * i] = __float_as_uint(m.x);
+            u[2 * i + 1] = __float_as_uint(m.y);
+        }
+        tmem_st16(taddr + k * 16, u);
     }
 }
 
@@ -225,7 +236,9 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t sr
 }
 
 template <typename T, int DA, int DB, bool STATE>
-__global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcParams P) {
+__global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcBatch Q) {
+    const LaTcParams& P = Q.core[blockIdx.x / (unsigned)Q.ctas];
+    const unsigned cta = blockIdx.x % (unsigned)Q.ctas;
     using Sh = LaShape<DA, DB>;
     constexpr bool kHalf = std::is_same<T, __half>::value;
     // f16 scores and decayed x are kept 16 and 64 times their size: the lo
@@ -242,7 +255,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     __shared__ float pw[kC + 2];    // decay^k
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int bh = (int)(blockIdx.x % (unsigned)P.BH), seg = (int)(blockIdx.x / (unsigned)P.BH);
+    const int bh = (int)(cta % (unsigned)P.BH), seg = (int)(cta / (unsigned)P.BH);
     const int b = bh / P.H, h = bh % P.H;
     const int len = P.lengths ? max(0, min(P.T, P.lengths[b])) : P.T;
     const int s0 = seg * P.seg_tokens, s1 = min(P.T, s0 + P.seg_tokens);
@@ -342,13 +355,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         const uint32_t ch = (uint32_t)(w4 & 1) * 4 + ((lane >> 3) & 1);
         const int j0 = g4 * 32 + 2 * (lane & 3);  // this lane's tokens of x: j0 + 8 m, + 1
 
-        // out of chunk c (P Y is done), staged in the place of a tile that
-        // nothing reads any more, this warp's 32 rows x kN columns of it
-        auto write_out = [&](int c, uint32_t place) {
+        // out of chunk c (v: its sums, read from TMEM), staged in the place of a
+        // tile that nothing reads any more, this warp's 32 rows x kN columns
+        auto write_out = [&](int c, uint32_t place, const float (&v)[kN]) {
             const int n = rows_of(chunk_at(c));
-            float v[kN];
-            tmem_ldn<kN>(lane_base + kTmemO + col0, v);
-            tmem_ld_wait();
             tc_fence_before();
             warp_arrive(o_free, lane);
             const float2 os = make_float2(P.oscale / kUp, P.oscale / kUp);
@@ -371,38 +381,32 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             if (lane == 0 && t < P.T && col0 < P.Db) tma_store_4d(&P.to, tile, col0, t, h, b);
         };
 
+        // this warp's part of M before the chunk at hand
+        float mv[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int col = col0 + i;
+            mv[i] = 0.f;
+            if (m_in && row < P.Da && col < P.Db) mv[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + row : (int64_t)row * P.Db + col];
+        }
+        auto rescale = [&] {  // what TMEM holds to M
+            if constexpr (kHalf)
+#pragma unroll
+                for (int i = 0; i < kN; ++i) mv[i] *= 1.f / kUpX;
+        };
         for (int c = 0; c < n_chunks; ++c) {
             const int n = rows_of(chunk_at(c));
             const int first = holds_end && c == 0 ? 1 : 0;
-            // ------------------------------------------------------- A: M
-            // (what is needed of the chunk before was waited for in its step C)
+            // ------------------------------------------------- A: M, and x
+            // (the chunk before's M has been read in its step C)
             if (STATE && c > 0) {
                 ok = waits(m_ready, c - 1, kErrEpilogue);
                 if (!ok) break;
                 tc_fence_after();
+                tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
+                tmem_ld_wait();
+                rescale();
             }
-            float mv[kN];
-            if (fed) {
-                if (c == 0) {
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        const int col = col0 + i;
-                        mv[i] = 0.f;
-                        if (m_in && row < P.Da && col < P.Db)
-                            mv[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + row : (int64_t)row * P.Db + col];
-                    }
-                } else {
-                    tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
-                    tmem_ld_wait();
-                    if constexpr (kHalf)
-#pragma unroll
-                        for (int i = 0; i < kN; ++i) mv[i] *= 1.f / kUpX;
-                }
-                uint32_t u[kN];
-                scaled<kN>(mv, pw[n - first] * kUpX, u);
-                tmem_stn<kN>(lane_base + kTmemM + col0, u);
-            }
-            // ----------------------------------------------- A: decayed x
             ok = waits(x_full[c & 1], c >> 1, kErrEpilogue);
             if (!ok) break;
             if (fed) {
@@ -418,10 +422,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     for (int k = 0; k < 2; ++k)
                         ldsm4_trans(xs + Sh::x(c) + k * 2048u + (((ch + ah * 2) ^ (lane & 7)) << 4), x[ah] + 4 * k);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    f[m] = ft[4 * m];
-                    if constexpr (kUpX != kUp) f[m] = __fmul2_rn(f[m], make_float2(kUpX / kUp, kUpX / kUp));
-                }
+                for (int m = 0; m < 4; ++m) f[m] = ft[4 * m];
+                tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
+                if constexpr (kUpX != kUp)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) f[m] = __fmul2_rn(f[m], make_float2(kUpX / kUp, kUpX / kUp));
 #pragma unroll
                 for (int ah = 0; ah < 2; ++ah) {
                     uint32_t u[16];  // hi, then lo
@@ -478,11 +483,18 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 ok = waits(s_ready, c, kErrEpilogue) && waits(a_done, c, kErrEpilogue);
                 if (!ok) break;
                 tc_fence_after();
-                if (c > 0) write_out(c - 1, Sh::x(c));
+                if (c > 0) {
+                    float v[kN];
+                    tmem_ldn<kN>(lane_base + kTmemO + col0, v);
+                    tmem_ld_wait();
+                    write_out(c - 1, Sh::x(c), v);
+                }
                 {
                     const int p0 = g4 * 32;  // columns of S
                     uint32_t u[32];          // hi, then lo
-                    if (P.reverse ? g4 < w4 : g4 > w4) {  // none of the 32 columns is seen by the 32 rows
+                    // whether any of the 32 columns is seen by any of the 32 rows
+                    const bool seen = P.reverse ? g4 >= w4 : g4 <= w4;
+                    if (!seen) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) u[i] = 0;
                     } else {
@@ -516,16 +528,16 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 {
                     const int w = P.reverse ? n - row - first : row + 1;
                     float v[kN];
-                    uint32_t u[kN];
                     tmem_ldn<kN>(lane_base + kTmemO + col0, v);
+                    tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
                     tmem_ld_wait();
                     // rows after the end may hold NaN; they are not stored
-                    scaled<kN>(v, row < n ? pw[w] * kUp : 0.f, u);
-                    tmem_stn<kN>(lane_base + kTmemO + col0, u);
+                    tmem_st_scaled<kN>(lane_base + kTmemO + col0, v, row < n ? pw[w] * kUp : 0.f);
                     tmem_st_wait();
                 }
                 tc_fence_before();
                 warp_arrive(p_done, lane);
+                rescale();
                 if (lane == 0) {
                     bulk_wait_read_all();  // X's place is free when out has left it
                     mbar_arrive(smem_u32(&x_free[c & 1]));
@@ -533,24 +545,29 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 __syncwarp();
             }
         }
-        if (ok && waits(m_ready, n_chunks - 1, kErrEpilogue)) {
-            tc_fence_after();
-            if (m_out && fed) {
-                float v[kN];
-                tmem_ldn<kN>(lane_base + kTmemM + col0, v);
+        if (STATE && ok) {
+            ok = waits(m_ready, n_chunks - 1, kErrEpilogue);
+            if (ok) {
+                tc_fence_after();
+                tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
                 tmem_ld_wait();
-                const float last = (P.reverse && P.final ? pw[1] : 1.f) / kUpX;
-                if (row < P.Da)
-#pragma unroll
-                    for (int i = 0; i < kN; ++i)
-                        if (col0 + i < P.Db) m_out[(int64_t)row * P.Db + col0 + i] = v[i] * last;
+                rescale();
             }
-            if constexpr (!STATE)
-                if (waits(o_ready, n_chunks - 1, kErrEpilogue)) {
-                    tc_fence_after();
-                    write_out(n_chunks - 1, Sh::x(n_chunks - 1));
-                }
         }
+        if (ok && m_out && row < P.Da) {
+            const float last = P.reverse && P.final ? pw[1] : 1.f;
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (col0 + i < P.Db) m_out[(int64_t)row * P.Db + col0 + i] = mv[i] * last;
+        }
+        if constexpr (!STATE)
+            if (ok && waits(o_ready, n_chunks - 1, kErrEpilogue)) {
+                tc_fence_after();
+                float v[kN];
+                tmem_ldn<kN>(lane_base + kTmemO + col0, v);
+                tmem_ld_wait();
+                write_out(n_chunks - 1, Sh::x(n_chunks - 1), v);
+            }
         if (!STATE && lane == 0) bulk_wait_all();
         __syncwarp();
         if constexpr (kHalf)
@@ -668,25 +685,37 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
 // The matrix before each segment from the segments' own sums, in place:
 // cur <- decay^n cur + sum, element by element along the walk; the last one is
 // the walk's result.
-__global__ void __launch_bounds__(256) la_chain(float* sums, const float* m_in, int m_in_t, float* m_out, const float* log_decay,
-                                                const int32_t* lengths, int reverse, int T, int H, int Da, int Db, int BH,
-                                                int seg_tokens, int segs) {
-    const int64_t msize = (int64_t)Da * Db, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= msize * BH) return;
+struct LaChain {
+    float* sums;
+    const float* m_in;
+    float* m_out;
+    int m_in_t, reverse, Da, Db;
+};
+struct LaChainBatch {
+    LaChain core[3];
+    const float* log_decay;
+    const int32_t* lengths;
+    int T, H, BH, seg_tokens, segs;
+};
+
+__global__ void __launch_bounds__(256) la_chain(const __grid_constant__ LaChainBatch Q) {
+    const LaChain& P = Q.core[blockIdx.y];
+    const int64_t msize = (int64_t)P.Da * P.Db, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= msize * Q.BH) return;
     const int bh = (int)(i / msize);
     const int64_t e = i % msize;
-    const int len = lengths ? max(0, min(T, lengths[bh / H])) : T;
-    const float g = fmaxf(log_decay[bh % H], -1e30f);
-    float cur = m_in ? m_in[bh * msize + (m_in_t ? (e % Db) * Da + e / Db : e)] : 0.f;
-    for (int k = 0; k < segs; ++k) {
-        const int seg = reverse ? segs - 1 - k : k, s0 = seg * seg_tokens;
-        const int n = max(0, min(len, min(T, s0 + seg_tokens)) - s0);
-        float* at = sums + seg * (int64_t)BH * msize + i;
+    const int len = Q.lengths ? max(0, min(Q.T, Q.lengths[bh / Q.H])) : Q.T;
+    const float g = fmaxf(Q.log_decay[bh % Q.H], -1e30f);
+    float cur = P.m_in ? P.m_in[bh * msize + (P.m_in_t ? (e % P.Db) * P.Da + e / P.Db : e)] : 0.f;
+    for (int k = 0; k < Q.segs; ++k) {
+        const int seg = P.reverse ? Q.segs - 1 - k : k, s0 = seg * Q.seg_tokens;
+        const int n = max(0, min(len, min(Q.T, s0 + Q.seg_tokens)) - s0);
+        float* at = P.sums + seg * (int64_t)Q.BH * msize + i;
         const float sum = *at;
         *at = cur;
-        if (n > 0) cur = fmaf(expf((float)(n - (reverse && s0 + n == len ? 1 : 0)) * g), cur, sum);
+        if (n > 0) cur = fmaf(expf((float)(n - (P.reverse && s0 + n == len ? 1 : 0)) * g), cur, sum);
     }
-    if (m_out) m_out[i] = reverse && len > 0 ? expf(g) * cur : cur;
+    if (P.m_out) P.m_out[i] = P.reverse && len > 0 ? expf(g) * cur : cur;
 }
 
 bool map_tensor(CUtensorMap* m, const LaCore& c, const void* p, const int64_t (&st)[3], int D, int cols = 64, int rows = kC) {
@@ -715,35 +744,41 @@ bool tma_ok(const LaCore& c, const void* p, const int64_t (&st)[3]) {
 }
 
 template <typename T, int DA, int DB, bool STATE>
-cudaError_t launch_k(const LaTcParams& P, cudaStream_t s) {
+cudaError_t launch_k(const LaTcBatch& Q, int cores, cudaStream_t s) {
     auto k = la_chunks<T, DA, DB, STATE>;
     constexpr int bytes = (int)LaShape<DA, DB>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)(P.BH * P.segs), kLaThreads, bytes, s>>>(P);
+    k<<<(unsigned)(Q.ctas * cores), kLaThreads, bytes, s>>>(Q);
     return cudaGetLastError();
 }
 
 template <typename T, bool STATE>
-cudaError_t launch_d(const LaTcParams& P, cudaStream_t s) {
-    if (P.Da <= 64) return P.Db <= 64 ? launch_k<T, 64, 64, STATE>(P, s) : launch_k<T, 64, 128, STATE>(P, s);
-    return P.Db <= 64 ? launch_k<T, 128, 64, STATE>(P, s) : launch_k<T, 128, 128, STATE>(P, s);
+cudaError_t launch_d(const LaTcBatch& Q, int cores, cudaStream_t s) {
+    const LaTcParams& P = Q.core[0];
+    if (P.Da <= 64) return P.Db <= 64 ? launch_k<T, 64, 64, STATE>(Q, cores, s) : launch_k<T, 64, 128, STATE>(Q, cores, s);
+    return P.Db <= 64 ? launch_k<T, 128, 64, STATE>(Q, cores, s) : launch_k<T, 128, 128, STATE>(Q, cores, s);
 }
 
 template <bool STATE>
-cudaError_t launch_t(const LaTcParams& P, int dtype, cudaStream_t s) {
-    return dtype == CT_BF16 ? launch_d<__nv_bfloat16, STATE>(P, s) : launch_d<__half, STATE>(P, s);
+cudaError_t launch_t(const LaTcBatch& Q, int cores, int dtype, cudaStream_t s) {
+    return dtype == CT_BF16 ? launch_d<__nv_bfloat16, STATE>(Q, cores, s) : launch_d<__half, STATE>(Q, cores, s);
 }
 
 // Segments of a sequence, and the tokens of one: as many as fill the GPU once
 // with one CTA each, of at least four chunks (a segment costs a second read of
 // X and Y and a chain step).
-void split(int64_t B, int64_t T, int64_t H, int sm_count, int* segs, int* tokens) {
+void split(int64_t heads, int64_t T, int sm_count, int* segs, int* tokens) {
     const int64_t chunks = (T + kC - 1) / kC;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(sm_count / std::max<int64_t>(1, B * H), chunks / 4));
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(sm_count / std::max<int64_t>(1, heads), chunks / 4));
     const int64_t per = (chunks + want - 1) / want;
     *tokens = (int)(per * kC);
     *segs = (int)((chunks + per - 1) / per);
+}
+
+size_t core_bytes(int64_t BH, int64_t msize, int segs, int dtype) {
+    const size_t m = (size_t)BH * msize * sizeof(float);
+    return (segs > 1 ? round256(m * segs) : 0) + (dtype == CT_F16 ? round256(m) + round256((size_t)BH * sizeof(int)) : 0);
 }
 
 }  // namespace
@@ -755,87 +790,114 @@ bool la_tc_fits(int64_t T, int64_t Dk, int64_t Dv, int dtype) {
 }
 
 bool la_tc_supports(const LaCore& c) {
-    return la_tc_fits(c.T, c.Da, c.Db, c.dtype) && c.B * c.H < (1ll << 24) && tma_ok(c, c.z, c.zs) && tma_ok(c, c.x, c.xs) &&
+    return la_tc_fits(c.T, c.Da, c.Db, c.dtype) && c.B * c.H < (1ll << 22) && tma_ok(c, c.z, c.zs) && tma_ok(c, c.x, c.xs) &&
            tma_ok(c, c.y, c.ys) && (!c.out || tma_ok(c, c.out, c.os));
 }
 
-size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype) {
+size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype, int backward) {
     if (!la_tc_fits(T, Dk, Dv, dtype)) return 0;
     DeviceInfo d;
-    int sm = 152, segs, tokens;
+    int sm = 152, tokens;
     if (device_info(&d) == cudaSuccess) sm = d.sm_count;
-    split(B, T, H, sm, &segs, &tokens);
-    const size_t m = (size_t)B * H * Dk * Dv * sizeof(float);
-    return (segs > 1 ? round256(m * segs) : 0) + (dtype == CT_F16 ? round256(m) + round256((size_t)B * H * sizeof(int)) : 0);
+    size_t most = 0;
+    // however many of the gradients are asked for
+    for (int cores = 1; cores <= (backward ? 3 : 1); ++cores) {
+        int segs;
+        split(B * H * cores, T, sm, &segs, &tokens);
+        most = std::max(most, cores * core_bytes(B * H, Dk * Dv, segs, dtype));
+    }
+    return most;
 }
 
-cudaError_t launch_la_tc(const LaCore& c, void* workspace, cudaStream_t s) {
+cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream_t s) {
     DeviceInfo d;
     cudaError_t e = device_info(&d);
     if (e != cudaSuccess) return e;
-    LaTcParams P;
-    std::memset(&P, 0, sizeof(P));
-    split(c.B, c.T, c.H, d.sm_count, &P.segs, &P.seg_tokens);
-    if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db) ||
-        (c.out && !map_tensor(&P.to, c, c.out, c.os, c.Db, c.Db <= 64 ? 16 : 32, 32)))
-        return cudaErrorInvalidValue;
-    const int64_t BH = c.B * c.H, msize = (int64_t)c.Da * c.Db;
-    char* ws = static_cast<char*>(workspace);
-    float* sums = nullptr;
-    if (P.segs > 1) {
-        sums = reinterpret_cast<float*>(ws);
-        ws += round256((size_t)BH * msize * P.segs * sizeof(float));
-    }
+    const LaCore& one = cores[0];
+    const int64_t BH = one.B * one.H, msize = (int64_t)one.Da * one.Db;
+    int segs, seg_tokens;
+    split(BH * n, one.T, d.sm_count, &segs, &seg_tokens);
     // f16: results are kept aside until it is known that no value left the
     // type's range (state_out may be state_in, which the second try reads)
-    float* m_out = c.m_out;
-    int* flags = nullptr;
-    if (c.dtype == CT_F16) {
-        if (c.m_out) m_out = reinterpret_cast<float*>(ws);
-        ws += round256((size_t)BH * msize * sizeof(float));
-        flags = reinterpret_cast<int*>(ws);
-        e = cudaMemsetAsync(flags, 0, (size_t)BH * sizeof(int), s);
-        if (e != cudaSuccess) return e;
+    int* flags[3] = {};
+    float* kept[3] = {};
+    LaTcBatch Q;
+    LaChainBatch C;
+    std::memset(&Q, 0, sizeof(Q));
+    std::memset(&C, 0, sizeof(C));
+    Q.ctas = (int)(BH * segs);
+    C.log_decay = one.log_decay;
+    C.lengths = one.lengths;
+    C.T = one.T;
+    C.H = one.H;
+    C.BH = (int)BH;
+    C.seg_tokens = seg_tokens;
+    C.segs = segs;
+    char* ws = static_cast<char*>(workspace);
+    for (int i = 0; i < n; ++i) {
+        const LaCore& c = cores[i];
+        LaTcParams& P = Q.core[i];
+        if (!map_tensor(&P.tz, c, c.z, c.zs, c.Da) || !map_tensor(&P.tx, c, c.x, c.xs, c.Da) || !map_tensor(&P.ty, c, c.y, c.ys, c.Db) ||
+            (c.out && !map_tensor(&P.to, c, c.out, c.os, c.Db, c.Db <= 64 ? 16 : 32, 32)))
+            return cudaErrorInvalidValue;
+        C.core[i] = {nullptr, c.m_in, c.m_out, c.m_in_t, c.reverse, c.Da, c.Db};
+        if (segs > 1) {
+            C.core[i].sums = reinterpret_cast<float*>(ws);
+            ws += round256((size_t)BH * msize * segs * sizeof(float));
+        }
+        if (c.dtype == CT_F16) {
+            if (c.m_out) kept[i] = C.core[i].m_out = reinterpret_cast<float*>(ws);
+            ws += round256((size_t)BH * msize * sizeof(float));
+            flags[i] = reinterpret_cast<int*>(ws);
+            ws += round256((size_t)BH * sizeof(int));
+            e = cudaMemsetAsync(flags[i], 0, (size_t)BH * sizeof(int), s);
+            if (e != cudaSuccess) return e;
+        }
+        P.out = c.out;
+        for (int k = 0; k < 3; ++k) P.os[k] = c.os[k];
+        P.log_decay = c.log_decay;
+        P.lengths = c.lengths;
+        P.flags = flags[i];
+        P.mscale = c.mscale;
+        P.oscale = c.oscale;
+        P.reverse = c.reverse;
+        P.T = c.T;
+        P.H = c.H;
+        P.Da = c.Da;
+        P.Db = c.Db;
+        P.BH = (int)BH;
+        P.segs = segs;
+        P.seg_tokens = seg_tokens;
+        P.wait_ns = wait_limit_ns();
+        const uint32_t type = c.dtype == CT_BF16 ? 1u : 0u;
+        const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(128 >> 4) << 24);  // D f32, M = 128
+        P.idesc_s = common | ((uint32_t)(kC >> 3) << 17);
+        P.idesc_n = common | (1u << 16) | ((uint32_t)((c.Db <= 64 ? 64 : 128) >> 3) << 17);
+        if (segs > 1) {
+            P.m_out = C.core[i].sums;
+        } else {
+            P.m_in = c.m_in;
+            P.m_in_t = c.m_in_t;
+            P.m_out = C.core[i].m_out;
+            P.final = 1;
+        }
     }
-    P.out = c.out;
-    for (int i = 0; i < 3; ++i) P.os[i] = c.os[i];
-    P.log_decay = c.log_decay;
-    P.lengths = c.lengths;
-    P.flags = flags;
-    P.mscale = c.mscale;
-    P.oscale = c.oscale;
-    P.reverse = c.reverse;
-    P.T = c.T;
-    P.H = c.H;
-    P.Da = c.Da;
-    P.Db = c.Db;
-    P.BH = (int)BH;
-    P.wait_ns = wait_limit_ns();
-    const uint32_t type = c.dtype == CT_BF16 ? 1u : 0u;
-    const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(128 >> 4) << 24);  // D f32, M = 128
-    P.idesc_s = common | ((uint32_t)(kC >> 3) << 17);
-    P.idesc_n = common | (1u << 16) | ((uint32_t)((c.Db <= 64 ? 64 : 128) >> 3) << 17);
-    if (P.segs > 1) {
-        P.m_out = sums;
-        e = launch_t<true>(P, c.dtype, s);
+    if (segs > 1) {
+        e = launch_t<true>(Q, n, one.dtype, s);
         if (e != cudaSuccess) return e;
-        la_chain<<<(unsigned)((BH * msize + 255) / 256), 256, 0, s>>>(sums, c.m_in, c.m_in_t, m_out, c.log_decay, c.lengths, c.reverse,
-                                                                     c.T, c.H, c.Da, c.Db, (int)BH, P.seg_tokens, P.segs);
+        la_chain<<<dim3((unsigned)((BH * msize + 255) / 256), n), 256, 0, s>>>(C);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        P.m_in = sums;
-        P.m_in_seg = 1;
-        P.m_out = nullptr;
-    } else {
-        P.m_in = c.m_in;
-        P.m_in_t = c.m_in_t;
-        P.m_out = m_out;
-        P.final = 1;
+        for (int i = 0; i < n; ++i) {
+            Q.core[i].m_in = C.core[i].sums;
+            Q.core[i].m_in_seg = 1;
+            Q.core[i].m_out = nullptr;
+        }
     }
-    if (c.out) e = launch_t<false>(P, c.dtype, s);
-    else if (P.segs == 1) e = launch_t<true>(P, c.dtype, s);  // only the last matrix is asked for
-    if (e != cudaSuccess || !flags) return e;
-    return launch_la_scan(c, s, flags, m_out);
+    if (one.out) e = launch_t<false>(Q, n, one.dtype, s);
+    else if (segs == 1) e = launch_t<true>(Q, n, one.dtype, s);  // only the last matrix is asked for
+    for (int i = 0; i < n && e == cudaSuccess && flags[i]; ++i) e = launch_la_scan(cores[i], s, flags[i], kept[i]);
+    return e;
 }
 
 cudaError_t la_error_word(unsigned int* v, bool clear) {
