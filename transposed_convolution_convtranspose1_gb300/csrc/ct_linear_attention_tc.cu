@@ -107,13 +107,33 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block) {
     return d;
 }
 
-// D (+)= A B with A (16-bit, two consecutive K in a column) in TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// MMAs issued by one lane of a converged warp: the branch is inside, so that
+// descriptors and addresses stay in uniform registers (under `if (lane == 0)`
+// each MMA cost its thread about 75 cycles of moves into them).
+__device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D += A B with A (16-bit, two consecutive K in a column) in TMEM.
+__device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t& bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(&bar))
         : "memory");
 }
 
@@ -611,67 +631,63 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         __syncwarp();
     } else {
         // ------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            auto wait1 = [&](uint64_t& bar, int parity) {
-                return mbar_wait(smem_u32(&bar), (uint32_t)parity & 1u, kErrMma, &abort_flag, P.wait_ns);
-            };
-            // D += A B over the chunk's tokens, A = hi + lo in TMEM
-            auto by_y = [&](uint32_t d, uint32_t at, int c) {
-                const uint64_t yd = desc_mn(base + Sh::y(c), 16384);
-#pragma unroll 4
-                for (int k = 0; k < kC / 16; ++k) {
-                    const uint32_t ad = at + (k / 2) * 32 + (k & 1) * 8;
-                    mma_ts(d, ad, yd + 128 * k, P.idesc_n, 1);
-                    mma_ts(d, ad + 16, yd + 128 * k, P.idesc_n, 1);
-                }
-            };
-            for (int c = 0; c < n_chunks; ++c) {
-                const int s = c & 1;
-                if constexpr (!STATE) {
-                    const uint32_t zs = base + Sh::z(c), xs = base + Sh::x(c);
-                    if (!wait1(z_full[s], c >> 1) || !wait1(x_full[s], c >> 1)) break;
-                    // P of the chunk before has been multiplied: its place takes S
-                    if (c > 0 && !wait1(o_ready, c - 1)) break;
-                    tc_fence_after();
-#pragma unroll 4
-                    for (int k = 0; k < DA / 16; ++k) {
-                        const uint32_t o = (k / 4) * 16384u;
-                        mma_f16(tmem + kTmemP, smem_desc_sw128(zs + o) + 2 * (k & 3), smem_desc_sw128(xs + o) + 2 * (k & 3), P.idesc_s,
-                                k > 0);
-                    }
-                    mma_commit(smem_u32(&s_ready));
-                    mma_commit(smem_u32(&x_free[s]));
-                }
-                if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
-                tc_fence_after();
-                by_y(tmem + kTmemM, tmem + kTmemX, c);
-                if constexpr (!STATE) {
-                    if (!wait1(m_done, c)) break;
-                    if (c > 0 && !wait1(o_free, c - 1)) break;
-                    tc_fence_after();
-                    const uint32_t zs = base + Sh::z(c);
-                    const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
-#pragma unroll 4
-                    for (int k = 0; k < DA / 16; ++k) {
-                        const uint64_t ad = smem_desc_sw128(zs + (k / 4) * 16384u) + 2 * (k & 3);
-                        mma_f16(tmem + kTmemO, ad, mh + 128 * k, P.idesc_n, k > 0);
-                        mma_f16(tmem + kTmemO, ad, ml + 128 * k, P.idesc_n, 1);
-                    }
-                    mma_commit(smem_u32(&z_free[s]));
-                    mma_commit(smem_u32(&m_ready));  // the new M and Z M
-                    if (!wait1(p_done, c)) break;
-                    tc_fence_after();
-                    by_y(tmem + kTmemO, tmem + kTmemP, c);
-                    mma_commit(smem_u32(&o_ready));
-                } else {
-                    mma_commit(smem_u32(&m_ready));
-                }
-                mma_commit(smem_u32(&y_free[s]));
+        // the whole warp walks and waits; one elected lane issues
+        auto wait1 = [&](uint64_t& bar, int parity) { return waits(bar, parity, kErrMma); };
+        // D += A B over the chunk's tokens, A = hi + lo in TMEM
+        auto by_y = [&](uint32_t d, uint32_t at, int c) {
+            const uint64_t yd = desc_mn(base + Sh::y(c), 16384);
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k) {
+                const uint32_t ad = at + (k / 2) * 32 + (k & 1) * 8;
+                mma_ts_one(d, ad, yd + 128 * k, P.idesc_n);
+                mma_ts_one(d, ad + 16, yd + 128 * k, P.idesc_n);
             }
-            // no MMA may be in flight when TMEM is released
-            mma_commit(smem_u32(&drain_bar));
-            mbar_drain(smem_u32(&drain_bar), 0);
+        };
+        for (int c = 0; c < n_chunks; ++c) {
+            const int s = c & 1;
+            if constexpr (!STATE) {
+                const uint64_t zd = smem_desc_sw128(base + Sh::z(c)), xd = smem_desc_sw128(base + Sh::x(c));
+                if (!wait1(z_full[s], c >> 1) || !wait1(x_full[s], c >> 1)) break;
+                // P of the chunk before has been multiplied: its place takes S
+                if (c > 0 && !wait1(o_ready, c - 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < DA / 16; ++k) {
+                    const uint32_t o = (k / 4) * 1024 + (k & 3) * 2;  // 64 columns on: 16384 bytes; 16: 32 bytes
+                    mma_ss_one(tmem + kTmemP, zd + o, xd + o, P.idesc_s, k > 0);
+                }
+                commit_one(s_ready);
+                commit_one(x_free[s]);
+            }
+            if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
+            tc_fence_after();
+            by_y(tmem + kTmemM, tmem + kTmemX, c);
+            if constexpr (!STATE) {
+                if (!wait1(m_done, c)) break;
+                if (c > 0 && !wait1(o_free, c - 1)) break;
+                tc_fence_after();
+                const uint64_t zd = smem_desc_sw128(base + Sh::z(c));
+                const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
+#pragma unroll
+                for (int k = 0; k < DA / 16; ++k) {
+                    const uint32_t o = (k / 4) * 1024 + (k & 3) * 2;
+                    mma_ss_one(tmem + kTmemO, zd + o, mh + 128 * k, P.idesc_n, k > 0);
+                    mma_ss_one(tmem + kTmemO, zd + o, ml + 128 * k, P.idesc_n, 1);
+                }
+                commit_one(z_free[s]);
+                commit_one(m_ready);  // the new M and Z M
+                if (!wait1(p_done, c)) break;
+                tc_fence_after();
+                by_y(tmem + kTmemO, tmem + kTmemP, c);
+                commit_one(o_ready);
+            } else {
+                commit_one(m_ready);
+            }
+            commit_one(y_free[s]);
         }
+        // no MMA may be in flight when TMEM is released
+        commit_one(drain_bar);
+        mbar_drain(smem_u32(&drain_bar), 0);
         __syncwarp();
     }
 
