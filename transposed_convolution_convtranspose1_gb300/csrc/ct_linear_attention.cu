@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A, const int* only
     T* out = static_cast<T*>(A.out) + b * A.os[0] + h * A.os[2];
     const int64_t msize = (int64_t)A.Da * A.Db;
     if (only && !only[bh]) {
-        if (A.m_out)
+        if (kept)
             for (int i = tid; i < A.Da * kCols; i += kWarps * 32) {
                 const int c = b0 + i % kCols;
                 if (c < A.Db) A.m_out[bh * msize + (int64_t)(i / kCols) * A.Db + c] = kept[bh * msize + (int64_t)(i / kCols) * A.Db + c];

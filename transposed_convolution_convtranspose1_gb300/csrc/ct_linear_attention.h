@@ -44,7 +44,7 @@ constexpr int kLaScanTokens = 32;
 
 // Token by token on CUDA cores, the matrix in registers
 // (ct_linear_attention.cu).  With `only` ([B * H]) the heads whose flag is 0
-// are left alone but for m_out, which is copied from `kept`.
+// are left alone but for m_out, which is copied from `kept` where given.
 cudaError_t launch_la_scan(const LaCore& c, cudaStream_t stream, const int* only = nullptr, const float* kept = nullptr);
 
 // In chunks on the tensor cores (ct_linear_attention_tc.cu): 16-bit types,

@@ -271,7 +271,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     __shared__ uint64_t s_ready, m_ready, a_done, m_done, p_done, o_ready, o_free, drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ __align__(8) float tab[2][2 * kC];   // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]: one later
+    // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]:
+    // one later, for aligned pairs, half the banks on (lanes take both in turn)
+    __shared__ __align__(8) float tab[2][2 * kC + 16];
     __shared__ float pw[kC + 2];    // decay^k
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -349,6 +351,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // decayed x of chunk c; without S its place serves every second chunk, so
+    // that x is made ready while the chunk before is multiplied
+    auto x_at = [&](int c) { return STATE && (c & 1) ? kTmemP : kTmemX; };
     auto chunk_at = [&](int c) { return P.reverse ? n_chunks - 1 - c : c; };
     auto rows_of = [&](int k) { return min(kC, n_tok - k * kC); };
     auto waits = [&](uint64_t& bar, int parity, unsigned code) {
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     if (warp < kLaWorkers) {
         const int w4 = warp & 3, g4 = warp >> 2;
         const int row = w4 * 32 + lane, col0 = g4 * kN;
-        const bool fed = w4 * 32 < DA;  // columns of X feed this lane quarter of the decayed x and of M
+        const bool fed = DA == 128 || w4 * 32 < DA;  // columns of X feed this lane quarter of the decayed x and of M
         [[maybe_unused]] float top = 0.f;
         bool ok = true;
         if (!fed) {
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
 #pragma unroll
             for (int i = 0; i < 32; ++i) zero[i] = 0;
             tmem_st32(lane_base + kTmemX + g4 * 32, zero);
+            if (STATE) tmem_st32(lane_base + kTmemP + g4 * 32, zero);
             tmem_stn<kN>(lane_base + kTmemM + col0, zero);
             tmem_st_wait();
         }
@@ -401,6 +407,41 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             if (lane == 0 && t < P.T && col0 < P.Db) tma_store_4d(&P.to, tile, col0, t, h, b);
         };
 
+        // P of chunk c with n tokens, from S in its place
+        auto make_p = [&](int n) {
+            tc_fence_after();
+            const int p0 = g4 * 32;  // columns of S
+            uint32_t u[32];          // hi, then lo
+            // whether any of the 32 columns is seen by any of the 32 rows
+            const bool seen = P.reverse ? g4 >= w4 : g4 <= w4;
+            if (!seen) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = 0;
+            } else {
+                float v[32];
+                tmem_ld32(lane_base + kTmemP + p0, v);
+                tmem_ld_wait();
+                const int at = (kC - 1) + p0 - row;
+                const float2* f = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f[i]);
+                    v[2 * i] = m.x;
+                    v[2 * i + 1] = m.y;
+                }
+                if (n < kC)  // rows after the end hold anything, NaN included
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (row >= n || p0 + i >= n || (P.reverse ? p0 + i < row : p0 + i > row)) v[i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    split2<T>(make_float2(v[2 * i], v[2 * i + 1]), u[i], u[16 + i]);
+                    if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+                }
+            }
+            tmem_st32(lane_base + kTmemP + p0, u);
+        };
+
         // this warp's part of M before the chunk at hand
         float mv[kN];
 #pragma unroll
@@ -419,14 +460,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             const int first = holds_end && c == 0 ? 1 : 0;
             // ------------------------------------------------- A: M, and x
             // (the chunk before's M has been read in its step C)
-            if (STATE && c > 0) {
-                ok = waits(m_ready, c - 1, kErrEpilogue);
-                if (!ok) break;
-                tc_fence_after();
-                tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
-                tmem_ld_wait();
-                rescale();
-            }
             ok = waits(x_full[c & 1], c >> 1, kErrEpilogue);
             if (!ok) break;
             if (fed) {
@@ -443,7 +476,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                         ldsm4_trans(xs + Sh::x(c) + k * 2048u + (((ch + ah * 2) ^ (lane & 7)) << 4), x[ah] + 4 * k);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) f[m] = ft[4 * m];
-                tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
+                if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
                 if constexpr (kUpX != kUp)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) f[m] = __fmul2_rn(f[m], make_float2(kUpX / kUp, kUpX / kUp));
@@ -460,11 +493,23 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                         split2<T>(v, u[r], u[8 + r]);
                         if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
                     }
-                    tmem_st_16x32(lane_base + ((uint32_t)(ah * 16) << 16) + kTmemX + g4 * 32, u);
+                    tmem_st_16x32(lane_base + ((uint32_t)(ah * 16) << 16) + x_at(c) + g4 * 32, u);
                 }
+                if (!STATE) tmem_st_wait();
+            }
+            if (STATE) {
+                warp_arrive(x_free[c & 1], lane);
+                if (c > 0) {
+                    ok = waits(m_ready, c - 1, kErrEpilogue);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
+                    tmem_ld_wait();
+                    rescale();
+                }
+                tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
                 tmem_st_wait();
             }
-            if (STATE) warp_arrive(x_free[c & 1], lane);
             if (n < kC) {  // rows of Y after the end meet factors of 0: they must be finite
                 ok = waits(y_full[c & 1], c >> 1, kErrEpilogue);
                 if (!ok) break;
@@ -498,9 +543,13 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 }
                 warp_arrive(m_done, lane);
                 // ---------------------------------------------- B: out, P
-                // S is issued when P Y of the chunk before is done; it and
-                // every warp's step A have read X
-                ok = waits(s_ready, c, kErrEpilogue) && waits(a_done, c, kErrEpilogue);
+                // S is issued when P Y of the chunk before is done; when every
+                // warp's step A is done too, nothing reads X any more.  Warps
+                // that had nothing to do in A take P first, the others out.
+                ok = waits(s_ready, c, kErrEpilogue);
+                if (!ok) break;
+                if (!fed) make_p(n);
+                ok = waits(a_done, c, kErrEpilogue);
                 if (!ok) break;
                 tc_fence_after();
                 if (c > 0) {
@@ -509,38 +558,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     tmem_ld_wait();
                     write_out(c - 1, Sh::x(c), v);
                 }
-                {
-                    const int p0 = g4 * 32;  // columns of S
-                    uint32_t u[32];          // hi, then lo
-                    // whether any of the 32 columns is seen by any of the 32 rows
-                    const bool seen = P.reverse ? g4 >= w4 : g4 <= w4;
-                    if (!seen) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = 0;
-                    } else {
-                        float v[32];
-                        tmem_ld32(lane_base + kTmemP + p0, v);
-                        tmem_ld_wait();
-                        const int at = (kC - 1) + p0 - row;
-                        const float2* f = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f[i]);
-                            v[2 * i] = m.x;
-                            v[2 * i + 1] = m.y;
-                        }
-                        if (n < kC)  // rows after the end hold anything, NaN included
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (row >= n || p0 + i >= n || (P.reverse ? p0 + i < row : p0 + i > row)) v[i] = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            split2<T>(make_float2(v[2 * i], v[2 * i + 1]), u[i], u[16 + i]);
-                            if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
-                        }
-                    }
-                    tmem_st32(lane_base + kTmemP + p0, u);
-                }
+                if (fed) make_p(n);
                 // --------------------------------------------- C: Z M
                 ok = waits(m_ready, c, kErrEpilogue);
                 if (!ok) break;
@@ -661,7 +679,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             }
             if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
             tc_fence_after();
-            by_y(tmem + kTmemM, tmem + kTmemX, c);
+            by_y(tmem + kTmemM, tmem + x_at(c), c);
             if constexpr (!STATE) {
                 if (!wait1(m_done, c)) break;
                 if (c > 0 && !wait1(o_free, c - 1)) break;
@@ -723,13 +741,20 @@ __global__ void __launch_bounds__(256) la_chain(const __grid_constant__ LaChainB
     const int len = Q.lengths ? max(0, min(Q.T, Q.lengths[bh / Q.H])) : Q.T;
     const float g = fmaxf(Q.log_decay[bh % Q.H], -1e30f);
     float cur = P.m_in ? P.m_in[bh * msize + (P.m_in_t ? (e % P.Db) * P.Da + e / P.Db : e)] : 0.f;
-    for (int k = 0; k < Q.segs; ++k) {
-        const int seg = P.reverse ? Q.segs - 1 - k : k, s0 = seg * Q.seg_tokens;
-        const int n = max(0, min(len, min(Q.T, s0 + Q.seg_tokens)) - s0);
-        float* at = P.sums + seg * (int64_t)Q.BH * msize + i;
-        const float sum = *at;
-        *at = cur;
-        if (n > 0) cur = fmaf(expf((float)(n - (P.reverse && s0 + n == len ? 1 : 0)) * g), cur, sum);
+    auto seg_of = [&](int k) { return P.reverse ? Q.segs - 1 - k : k; };
+    const int64_t step = (int64_t)Q.BH * msize;
+    for (int k0 = 0; k0 < Q.segs; k0 += 8) {  // eight loads in flight
+        float sum[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] = k0 + k < Q.segs ? P.sums[seg_of(k0 + k) * step + i] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k0 + k >= Q.segs) break;
+            const int seg = seg_of(k0 + k), s0 = seg * Q.seg_tokens;
+            const int n = max(0, min(len, min(Q.T, s0 + Q.seg_tokens)) - s0);
+            P.sums[seg * step + i] = cur;
+            if (n > 0) cur = fmaf(expf((float)(n - (P.reverse && s0 + n == len ? 1 : 0)) * g), cur, sum[k]);
+        }
     }
     if (P.m_out) P.m_out[i] = P.reverse && len > 0 ? expf(g) * cur : cur;
 }
@@ -833,8 +858,9 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
     const int64_t BH = one.B * one.H, msize = (int64_t)one.Da * one.Db;
     int segs, seg_tokens;
     split(BH * n, one.T, d.sm_count, &segs, &seg_tokens);
-    // f16: results are kept aside until it is known that no value left the
-    // type's range (state_out may be state_in, which the second try reads)
+    // f16: a last matrix that takes the first one's place is kept aside until
+    // it is known that no value left the type's range (the second try reads
+    // the first one)
     int* flags[3] = {};
     float* kept[3] = {};
     LaTcBatch Q;
@@ -862,7 +888,7 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
             ws += round256((size_t)BH * msize * segs * sizeof(float));
         }
         if (c.dtype == CT_F16) {
-            if (c.m_out) kept[i] = C.core[i].m_out = reinterpret_cast<float*>(ws);
+            if (c.m_out && c.m_out == c.m_in) kept[i] = C.core[i].m_out = reinterpret_cast<float*>(ws);
             ws += round256((size_t)BH * msize * sizeof(float));
             flags[i] = reinterpret_cast<int*>(ws);
             ws += round256((size_t)BH * sizeof(int));
