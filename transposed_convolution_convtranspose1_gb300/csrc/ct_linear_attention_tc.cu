@@ -56,7 +56,7 @@ using namespace tcg;
 constexpr int kC = 128;            // tokens of a chunk
 constexpr int kLaWorkers = 16;     // warps
 constexpr int kLaThreads = (kLaWorkers + 2) * 32;
-constexpr uint32_t kTmemP = 0, kTmemX = 128, kTmemO = 256, kTmemM = 384;
+constexpr uint32_t kTmemP = 0, kTmemP2 = 256, kTmemX = 128;
 constexpr float kF16Max = 65504.f;
 
 struct LaTcParams {
@@ -266,9 +266,13 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // them the flag has the head done again
     constexpr float kUp = kHalf ? 16.f : 1.f, kUpX = kHalf ? 64.f : 1.f;
     constexpr int kN = DB / 4;  // columns of Y, M and out a warp has
+    // 64 columns of out and M leave room for a second S: the next chunk's is
+    // formed before P Y of this one
+    constexpr bool kTwoS = DB == 64;
+    constexpr uint32_t kTmemO = kTwoS ? 384 : 256, kTmemM = kTwoS ? 448 : 384;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t z_full[2], x_full[2], y_full[2], z_free[2], x_free[2], y_free[2];
-    __shared__ uint64_t s_ready, m_ready, a_done, m_done, p_done, o_ready, o_free, drain_bar;
+    __shared__ uint64_t x_full[2], y_full[2], z_free[2], x_free[2], y_free[2];  // x_full: Z and X
+    __shared__ uint64_t s_ready, m_ready, a_done, p_done, o_ready, o_free, drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]:
@@ -316,7 +320,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&z_full[i]), 1);
             mbar_init(smem_u32(&y_full[i]), 1);
             mbar_init(smem_u32(&y_free[i]), 1);
             mbar_init(smem_u32(&z_free[i]), 1);
@@ -325,7 +328,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         }
         mbar_init(smem_u32(&s_ready), 1);
         mbar_init(smem_u32(&a_done), kLaWorkers);
-        mbar_init(smem_u32(&m_done), kLaWorkers);
         mbar_init(smem_u32(&p_done), kLaWorkers);
         mbar_init(smem_u32(&o_ready), 1);
         mbar_init(smem_u32(&m_ready), 1);
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // decayed x of chunk c; without S its place serves every second chunk, so
     // that x is made ready while the chunk before is multiplied
     auto x_at = [&](int c) { return STATE && (c & 1) ? kTmemP : kTmemX; };
+    auto p_at = [&](int c) { return kTwoS && (c & 1) ? kTmemP2 : kTmemP; };
     auto chunk_at = [&](int c) { return P.reverse ? n_chunks - 1 - c : c; };
     auto rows_of = [&](int k) { return min(kC, n_tok - k * kC); };
     auto waits = [&](uint64_t& bar, int parity, unsigned code) {
@@ -382,7 +385,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         const int j0 = g4 * 32 + 2 * (lane & 3);  // this lane's tokens of x: j0 + 8 m, + 1
 
         // out of chunk c (v: its sums, read from TMEM), staged in the place of a
-        // tile that nothing reads any more, this warp's 32 rows x kN columns
+        // tile that nothing reads any more, this warp's 32 rows x kN columns.
+        // o_free then lets Z M of the chunk after begin: out's place is free
+        // and this warp's part of M is in shared memory.
         auto write_out = [&](int c, uint32_t place, const float (&v)[kN]) {
             const int n = rows_of(chunk_at(c));
             tc_fence_before();
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         };
 
         // P of chunk c with n tokens, from S in its place
-        auto make_p = [&](int n) {
+        auto make_p = [&](int c, int n) {
             tc_fence_after();
             const int p0 = g4 * 32;  // columns of S
             uint32_t u[32];          // hi, then lo
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 for (int i = 0; i < 32; ++i) u[i] = 0;
             } else {
                 float v[32];
-                tmem_ld32(lane_base + kTmemP + p0, v);
+                tmem_ld32(lane_base + p_at(c) + p0, v);
                 tmem_ld_wait();
                 const int at = (kC - 1) + p0 - row;
                 const float2* f = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
                 }
             }
-            tmem_st32(lane_base + kTmemP + p0, u);
+            tmem_st32(lane_base + p_at(c) + p0, u);
         };
 
         // this warp's part of M before the chunk at hand
@@ -460,7 +465,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             const int first = holds_end && c == 0 ? 1 : 0;
             // ------------------------------------------------- A: M, and x
             // (the chunk before's M has been read in its step C)
-            ok = waits(x_full[c & 1], c >> 1, kErrEpilogue);
+            // (with two places for S it was formed long ago, of the loaded X)
+            ok = !STATE && kTwoS ? waits(s_ready, c, kErrEpilogue) : waits(x_full[c & 1], c >> 1, kErrEpilogue);
             if (!ok) break;
             if (fed) {
                 // the factors of the last row forward in time (0 for tokens
@@ -541,24 +547,31 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     }
                     fence_async_smem();
                 }
-                warp_arrive(m_done, lane);
                 // ---------------------------------------------- B: out, P
-                // S is issued when P Y of the chunk before is done; when every
-                // warp's step A is done too, nothing reads X any more.  Warps
-                // that had nothing to do in A take P first, the others out.
-                ok = waits(s_ready, c, kErrEpilogue);
-                if (!ok) break;
-                if (!fed) make_p(n);
+                // With S formed and every warp's step A done nothing reads X
+                // any more.  Warps that had nothing to do in A take P first,
+                // the others out.
+                if (!kTwoS) {
+                    ok = waits(s_ready, c, kErrEpilogue);
+                    if (!ok) break;
+                }
+                if (!fed) make_p(c, n);
                 ok = waits(a_done, c, kErrEpilogue);
                 if (!ok) break;
-                tc_fence_after();
                 if (c > 0) {
+                    if (kTwoS) {  // (one place for S: it is free, so P Y is done)
+                        ok = waits(o_ready, c - 1, kErrEpilogue);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
                     float v[kN];
                     tmem_ldn<kN>(lane_base + kTmemO + col0, v);
                     tmem_ld_wait();
                     write_out(c - 1, Sh::x(c), v);
+                } else {
+                    warp_arrive(o_free, lane);
                 }
-                if (fed) make_p(n);
+                if (fed) make_p(c, n);
                 // --------------------------------------------- C: Z M
                 ok = waits(m_ready, c, kErrEpilogue);
                 if (!ok) break;
@@ -613,35 +626,31 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     } else if (warp == kLaWorkers) {
         // ------------------------------------------------------- TMA loads
         if (lane == 0) {
-            int nz = 0, nx = 0, ny = 0;  // fills issued
+            int nx = 0, ny = 0;  // fills issued
             bool ok = true;
             auto fill = [&](const CUtensorMap* map, uint64_t& full, uint32_t place, int D, int t0) {
-                mbar_expect_tx(smem_u32(&full), 256 * D);
                 for (int k = 0; k < D / 64; ++k) tma_load_4d(base + place + k * 16384u, map, smem_u32(&full), k * 64, t0, h, b);
             };
             // a place was last used by the tile five before: X of two chunks
             // ago for Z, Y of two chunks ago for X, the last chunk's Z for Y
             for (int c = 0; c < n_chunks; ++c) {
                 const int t0 = s0 + chunk_at(c) * kC, s = c & 1;
-                ok = c < 2 || mbar_wait(smem_u32(&x_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
+                ok = c < 2 || (mbar_wait(smem_u32(&x_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns) &&
+                               mbar_wait(smem_u32(&y_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns));
                 if (!ok) break;
-                if (!STATE) {
-                    fill(&P.tz, z_full[s], Sh::z(c), DA, t0);
-                    ++nz;
-                }
-                ok = c < 2 || mbar_wait(smem_u32(&y_free[s]), ((c >> 1) - 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
-                if (!ok) break;
+                mbar_expect_tx(smem_u32(&x_full[s]), 256 * DA * (STATE ? 1 : 2));
+                if (!STATE) fill(&P.tz, x_full[s], Sh::z(c), DA, t0);
                 fill(&P.tx, x_full[s], Sh::x(c), DA, t0);
                 ++nx;
                 ok = STATE || c < 1 || mbar_wait(smem_u32(&z_free[s ^ 1]), ((c - 1) >> 1) & 1, kErrProducer, &abort_flag, P.wait_ns);
                 if (!ok) break;
+                mbar_expect_tx(smem_u32(&y_full[s]), 256 * DB);
                 fill(&P.ty, y_full[s], Sh::y(c), DB, t0);
                 ++ny;
             }
             if (!ok) {
                 // what was issued must land before the CTA exits: the last
                 // fill of each barrier
-                for (int i = max(0, nz - 2); i < nz; ++i) mbar_drain(smem_u32(&z_full[i & 1]), (i >> 1) & 1);
                 for (int i = max(0, nx - 2); i < nx; ++i) mbar_drain(smem_u32(&x_full[i & 1]), (i >> 1) & 1);
                 for (int i = max(0, ny - 2); i < ny; ++i) mbar_drain(smem_u32(&y_full[i & 1]), (i >> 1) & 1);
             }
@@ -661,28 +670,31 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 mma_ts_one(d, ad + 16, yd + 128 * k, P.idesc_n);
             }
         };
-        for (int c = 0; c < n_chunks; ++c) {
-            const int s = c & 1;
-            if constexpr (!STATE) {
-                const uint64_t zd = smem_desc_sw128(base + Sh::z(c)), xd = smem_desc_sw128(base + Sh::x(c));
-                if (!wait1(z_full[s], c >> 1) || !wait1(x_full[s], c >> 1)) break;
-                // P of the chunk before has been multiplied: its place takes S
-                if (c > 0 && !wait1(o_ready, c - 1)) break;
-                tc_fence_after();
+        auto form_s = [&](int c) {  // false where a wait gave up
+            const uint64_t zd = smem_desc_sw128(base + Sh::z(c)), xd = smem_desc_sw128(base + Sh::x(c));
+            if (!wait1(x_full[c & 1], c >> 1)) return false;
+            // the P that was in its place has been multiplied
+            const int before = kTwoS ? c - 2 : c - 1;
+            if (before >= 0 && !wait1(o_ready, before)) return false;
+            tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < DA / 16; ++k) {
-                    const uint32_t o = (k / 4) * 1024 + (k & 3) * 2;  // 64 columns on: 16384 bytes; 16: 32 bytes
-                    mma_ss_one(tmem + kTmemP, zd + o, xd + o, P.idesc_s, k > 0);
-                }
-                commit_one(s_ready);
-                commit_one(x_free[s]);
+            for (int k = 0; k < DA / 16; ++k) {
+                const uint32_t o = (k / 4) * 1024 + (k & 3) * 2;  // 64 columns on: 16384 bytes; 16: 32 bytes
+                mma_ss_one(tmem + p_at(c), zd + o, xd + o, P.idesc_s, k > 0);
             }
+            commit_one(s_ready);
+            commit_one(x_free[c & 1]);
+            return true;
+        };
+        bool ok = STATE || form_s(0);
+        for (int c = 0; c < n_chunks && ok; ++c) {
+            const int s = c & 1;
+            if (!STATE && !kTwoS && c > 0 && !form_s(c)) break;
             if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
             tc_fence_after();
             by_y(tmem + kTmemM, tmem + x_at(c), c);
             if constexpr (!STATE) {
-                if (!wait1(m_done, c)) break;
-                if (c > 0 && !wait1(o_free, c - 1)) break;
+                if (!wait1(o_free, c)) break;
                 tc_fence_after();
                 const uint64_t zd = smem_desc_sw128(base + Sh::z(c));
                 const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
@@ -694,9 +706,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 }
                 commit_one(z_free[s]);
                 commit_one(m_ready);  // the new M and Z M
+                // (every warp has seen this chunk's s_ready: o_free follows it)
+                if (kTwoS && c + 1 < n_chunks && !form_s(c + 1)) break;
                 if (!wait1(p_done, c)) break;
                 tc_fence_after();
-                by_y(tmem + kTmemO, tmem + kTmemP, c);
+                by_y(tmem + kTmemO, tmem + p_at(c), c);
                 commit_one(o_ready);
             } else {
                 commit_one(m_ready);
