@@ -12,76 +12,122 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCols = 32;    // columns of M a block owns
-constexpr int kTokens = 16;  // tokens staged at a time
+
+struct ScanArgs {
+    LaCore c;
+    const int* only;         // heads with flag 0 are left alone ...
+    const float* kept;       // ... but for m_out, copied from here
+    int seg_tokens;          // of a segment (blockIdx.z)
+    int m_in_seg, m_out_seg; // a matrix for each segment; m_out: its own sum
+};
 
 // A block owns 32 columns of one head's matrix: columns of M never meet, so
 // the only sum across threads is out = M^T z over the rows.  Lane = 4 row
 // runs x 8 column quads, each thread RX consecutive rows x 4 columns in
-// registers; partial outputs are joined by two shuffles and, across the four
-// warps, through shared memory once per 16 tokens.
-template <typename T, int RX>
-__global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A, const int* only, const float* kept) {
-    constexpr int D = kWarps * 4 * RX;  // rows held (>= Da)
-    __shared__ __align__(16) float xs[kTokens][D];
-    __shared__ __align__(16) float zs[kTokens][D];
-    __shared__ __align__(16) float ys[kTokens][kCols];
-    __shared__ __align__(16) float part[kWarps][kTokens][kCols];
+// registers.  A token's partial sums are joined by three shuffles (each halves
+// the columns a lane still carries) and, across the four warps, through shared
+// memory once per TB tokens; the next TB tokens' values are on their way in
+// registers meanwhile.  A streaming step (one token) is bound by memory, the
+// state read and written: 64 x 8 heads of 128 x 128, 20 us (134 MB).  Longer
+// sequences are bound by each token's chain of sums.
+template <typename T, int RX, int TB>
+__global__ void __launch_bounds__(kWarps * 32) la_scan(const __grid_constant__ ScanArgs S) {
+    const LaCore& A = S.c;
+    constexpr int D = kWarps * 4 * RX, kThreads = kWarps * 32;  // D: rows held (>= Da)
+    constexpr int NX = TB * D / kThreads, NY = TB * kCols / kThreads;
+    __shared__ __align__(16) float xs[TB][D];
+    __shared__ __align__(16) float zs[TB][D];
+    __shared__ __align__(16) float ys[TB][kCols];
+    __shared__ __align__(16) float part[kWarps][TB][kCols];
     __shared__ float first_gamma;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane >> 3, c4 = (lane & 7) * 4;
     const int a0 = (warp * 4 + sub) * RX, b0 = blockIdx.y * kCols;
-    const int64_t bh = blockIdx.x;
+    const int64_t bh = blockIdx.x, BH = gridDim.x;
     const int b = (int)(bh / A.H), h = (int)(bh % A.H);
-    const int n = A.lengths ? max(0, min(A.T, A.lengths[b])) : A.T;
+    const int len = A.lengths ? max(0, min(A.T, A.lengths[b])) : A.T;
+    const int s0 = blockIdx.z * S.seg_tokens, s1 = min(A.T, s0 + S.seg_tokens);
+    const int n = max(0, min(len, s1) - s0);  // tokens of this segment
+    // backward in time the sequence's last token takes the matrix undecayed
+    const bool holds_end = A.reverse && n > 0 && s0 + n == len;
     // exp(0 * g) must be 1 for a decay of zero (g = -infinity) too
     const float gamma = expf(fmaxf(A.log_decay[h], -1e30f));
-    const T* z = static_cast<const T*>(A.z) + b * A.zs[0] + h * A.zs[2];
-    const T* x = static_cast<const T*>(A.x) + b * A.xs[0] + h * A.xs[2];
-    const T* y = static_cast<const T*>(A.y) + b * A.ys[0] + h * A.ys[2];
-    T* out = static_cast<T*>(A.out) + b * A.os[0] + h * A.os[2];
+    const T* z = static_cast<const T*>(A.z) + b * A.zs[0] + s0 * A.zs[1] + h * A.zs[2];
+    const T* x = static_cast<const T*>(A.x) + b * A.xs[0] + s0 * A.xs[1] + h * A.xs[2];
+    const T* y = static_cast<const T*>(A.y) + b * A.ys[0] + s0 * A.ys[1] + h * A.ys[2];
+    T* out = A.out ? static_cast<T*>(A.out) + b * A.os[0] + s0 * A.os[1] + h * A.os[2] : nullptr;
     const int64_t msize = (int64_t)A.Da * A.Db;
-    if (only && !only[bh]) {
-        if (kept)
-            for (int i = tid; i < A.Da * kCols; i += kWarps * 32) {
+    const float* m_in = A.m_in ? A.m_in + (bh + (S.m_in_seg ? blockIdx.z * BH : 0)) * msize : nullptr;
+    float* m_out = A.m_out ? A.m_out + (bh + (S.m_out_seg ? blockIdx.z * BH : 0)) * msize : nullptr;
+    if (S.only && !S.only[bh]) {
+        if (S.kept)
+            for (int i = tid; i < A.Da * kCols; i += kThreads) {
                 const int c = b0 + i % kCols;
-                if (c < A.Db) A.m_out[bh * msize + (int64_t)(i / kCols) * A.Db + c] = kept[bh * msize + (int64_t)(i / kCols) * A.Db + c];
+                const int64_t e = (int64_t)(i / kCols) * A.Db + c;
+                if (c < A.Db) m_out[e] = S.kept[bh * msize + e];
             }
         return;
     }
 
+    // four columns as one access where a row's quads lie on 16 bytes
+    const bool quads = A.Db % 4 == 0 && !A.m_in_t && ((uintptr_t)m_in | (uintptr_t)m_out) % 16 == 0;
     float m[RX][4];
 #pragma unroll
-    for (int i = 0; i < RX; ++i)
+    for (int i = 0; i < RX; ++i) {
+        const int a = a0 + i, c0 = b0 + c4;
+        if (quads) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m_in && a < A.Da && c0 < A.Db) v = *reinterpret_cast<const float4*>(m_in + (int64_t)a * A.Db + c0);
+            m[i][0] = v.x; m[i][1] = v.y; m[i][2] = v.z; m[i][3] = v.w;
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int a = a0 + i, c = b0 + c4 + j;
+            const int c = c0 + j;
             m[i][j] = 0.f;
-            if (A.m_in && a < A.Da && c < A.Db)
-                m[i][j] = A.m_in[bh * msize + (A.m_in_t ? (int64_t)c * A.Da + a : (int64_t)a * A.Db + c)];
+            if (m_in && a < A.Da && c < A.Db) m[i][j] = m_in[A.m_in_t ? (int64_t)c * A.Da + a : (int64_t)a * A.Db + c];
         }
-    // gamma is rounded, and its t-th power is off by t times that: 7e-6 of the
-    // result after 300 tokens.  So the first step of every further round of 16
-    // takes what makes the round's product exp(16 g).
-    if (tid == 0 && n > kTokens) {
-        const double e = gamma, e2 = e * e, e4 = e2 * e2, e8 = e4 * e4;
-        first_gamma = gamma > 1e-10f ? (float)(exp(16.0 * (double)A.log_decay[h]) / (e8 * e4 * e2 * e)) : gamma;
     }
-    for (int t0 = 0; t0 < n; t0 += kTokens) {
-        const int nt = min(kTokens, n - t0);
-        for (int i = tid; i < nt * D; i += kWarps * 32) {
-            const int t = i / D, a = i % D;
+    // gamma is rounded, and its t-th power is off by t times that: 7e-6 of the
+    // result after 300 tokens.  So the first step of every further round of TB
+    // takes what makes the round's product exp(TB g).
+    if (tid == 0 && n > TB) {
+        const double e = gamma, e2 = e * e, e4 = e2 * e2, e7 = e4 * e2 * e;
+        first_gamma = gamma > 1e-10f ? (float)(exp((double)TB * (double)A.log_decay[h]) / (TB == 16 ? e7 * e4 * e4 : e7)) : gamma;
+    }
+    float px[NX], pz[NX], py[NY];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int t = (i * kThreads + tid) / D, a = (i * kThreads + tid) % D;
             const int64_t tok = A.reverse ? n - 1 - (t0 + t) : t0 + t;
-            xs[t][a] = a < A.Da ? to_f32(x[tok * A.xs[1] + a]) : 0.f;
-            zs[t][a] = a < A.Da ? to_f32(z[tok * A.zs[1] + a]) : 0.f;
+            const bool in = t0 + t < n && a < A.Da;
+            px[i] = in ? to_f32(x[tok * A.xs[1] + a]) : 0.f;
+            pz[i] = in && out ? to_f32(z[tok * A.zs[1] + a]) : 0.f;
         }
-        for (int i = tid; i < nt * kCols; i += kWarps * 32) {
-            const int t = i / kCols, c = i % kCols;
+#pragma unroll
+        for (int i = 0; i < NY; ++i) {
+            const int t = (i * kThreads + tid) / kCols, c = (i * kThreads + tid) % kCols;
             const int64_t tok = A.reverse ? n - 1 - (t0 + t) : t0 + t;
-            ys[t][c] = b0 + c < A.Db ? to_f32(y[tok * A.ys[1] + b0 + c]) * A.mscale : 0.f;
+            py[i] = t0 + t < n && b0 + c < A.Db ? to_f32(y[tok * A.ys[1] + b0 + c]) * A.mscale : 0.f;
         }
+    };
+    if (n > 0) fetch(0);
+    for (int t0 = 0; t0 < n; t0 += TB) {
+        const int nt = min(TB, n - t0);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = i * kThreads + tid;
+            xs[e / D][e % D] = px[i];
+            zs[e / D][e % D] = pz[i];
+        }
+#pragma unroll
+        for (int i = 0; i < NY; ++i) ys[(i * kThreads + tid) / kCols][(i * kThreads + tid) % kCols] = py[i];
         __syncthreads();
+        if (t0 + TB < n) fetch(t0 + TB);
+#pragma unroll 4
         for (int t = 0; t < nt; ++t) {
-            const float g = t > 0 ? gamma : t0 > 0 ? first_gamma : A.reverse ? 1.f : gamma;
+            const float g = t > 0 ? gamma : t0 > 0 ? first_gamma : holds_end ? 1.f : gamma;
             float yv[4], acc[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -97,16 +143,17 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A, const int* only
                     acc[j] = fmaf(m[i][j], zv, acc[j]);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 8);
-                acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 16);
-                if (sub == 0) part[warp][t][c4 + j] = acc[j];
-            }
+            // lanes 8 apart keep two columns each, lanes 16 apart one
+            const bool odd = sub & 1, high = sub & 2;
+            float k0 = odd ? acc[2] : acc[0], k1 = odd ? acc[3] : acc[1];
+            k0 += __shfl_xor_sync(0xffffffffu, odd ? acc[0] : acc[2], 8);
+            k1 += __shfl_xor_sync(0xffffffffu, odd ? acc[1] : acc[3], 8);
+            const float k = (high ? k1 : k0) + __shfl_xor_sync(0xffffffffu, high ? k0 : k1, 16);
+            part[warp][t][c4 + (odd ? 2 : 0) + (high ? 1 : 0)] = k;
         }
         __syncthreads();
-        if (A.out)
-            for (int i = tid; i < nt * kCols; i += kWarps * 32) {
+        if (out)
+            for (int i = tid; i < nt * kCols; i += kThreads) {
                 const int t = i / kCols, c = i % kCols;
                 const int64_t tok = A.reverse ? n - 1 - (t0 + t) : t0 + t;
                 float s = 0.f;
@@ -114,44 +161,103 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(LaCore A, const int* only
                 for (int w = 0; w < kWarps; ++w) s += part[w][t][c];
                 if (b0 + c < A.Db) out[tok * A.os[1] + b0 + c] = from_f32<T>(s * A.oscale);
             }
-        // the next round's staging writes xs, ys and zs only, and its partial
-        // sums come after its own barrier
+        // the next round writes xs, ys and zs at once, which nothing reads
+        // any more, and its partial sums after its own barrier
     }
-    if (A.out)
-        for (int64_t i = tid; i < (int64_t)(A.T - n) * kCols; i += kWarps * 32) {
+    if (out)
+        for (int64_t i = tid; i < (int64_t)(s1 - s0 - n) * kCols; i += kThreads) {
             const int c = (int)(i % kCols);
             if (b0 + c < A.Db) out[(n + i / kCols) * A.os[1] + b0 + c] = from_f32<T>(0.f);
         }
-    if (A.m_out) {
-        const float g = A.reverse && n > 0 ? gamma : 1.f;
+    if (m_out) {
+        const float g = A.reverse && !S.m_out_seg && n > 0 ? gamma : 1.f;
 #pragma unroll
-        for (int i = 0; i < RX; ++i)
+        for (int i = 0; i < RX; ++i) {
+            if (a0 + i >= A.Da) continue;
+            float* to = m_out + (int64_t)(a0 + i) * A.Db + b0 + c4;
+            if (quads) {
+                if (b0 + c4 < A.Db) *reinterpret_cast<float4*>(to) = make_float4(g * m[i][0], g * m[i][1], g * m[i][2], g * m[i][3]);
+                continue;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (a0 + i < A.Da && b0 + c4 + j < A.Db)
-                    A.m_out[bh * msize + (int64_t)(a0 + i) * A.Db + b0 + c4 + j] = g * m[i][j];
+                if (b0 + c4 + j < A.Db) to[j] = g * m[i][j];
+        }
     }
 }
 
 template <typename T>
-cudaError_t launch_t(const LaCore& A, cudaStream_t s, const int* only, const float* kept) {
-    const dim3 grid((unsigned)(A.B * A.H), (unsigned)((A.Db + kCols - 1) / kCols));
-    if (A.Da <= 32) la_scan<T, 2><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
-    else if (A.Da <= 64) la_scan<T, 4><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
-    else if (A.Da <= 128) la_scan<T, 8><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
-    else la_scan<T, 16><<<grid, kWarps * 32, 0, s>>>(A, only, kept);
+cudaError_t launch_t(const ScanArgs& S, int segs, cudaStream_t s) {
+    const LaCore& A = S.c;
+    const dim3 grid((unsigned)(A.B * A.H), (unsigned)((A.Db + kCols - 1) / kCols), (unsigned)segs);
+    if (A.Da <= 32) la_scan<T, 2, 16><<<grid, kWarps * 32, 0, s>>>(S);
+    else if (A.Da <= 64) la_scan<T, 4, 16><<<grid, kWarps * 32, 0, s>>>(S);
+    else if (A.Da <= 128) la_scan<T, 8, 16><<<grid, kWarps * 32, 0, s>>>(S);
+    else la_scan<T, 16, 8><<<grid, kWarps * 32, 0, s>>>(S);
     return cudaGetLastError();
+}
+
+cudaError_t launch(const ScanArgs& S, int segs, cudaStream_t s) {
+    if (S.c.B * S.c.H == 0) return cudaSuccess;
+    switch (S.c.dtype) {
+        case CT_F32: return launch_t<float>(S, segs, s);
+        case CT_F16: return launch_t<__half>(S, segs, s);
+        default: return launch_t<__nv_bfloat16>(S, segs, s);
+    }
+}
+
+// Segments of the scan and the tokens of one: enough to bring about four
+// blocks to an SM, of at least 64 tokens (a segment's first pass costs about
+// 2/3 of its second, so fewer tokens than that gain nothing).
+void scan_split(int64_t BH, int64_t T, int64_t Db, int* segs, int* tokens) {
+    const int64_t blocks = std::max<int64_t>(1, BH * ((Db + kCols - 1) / kCols));
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(608 / blocks, T / 64), 4096));
+    *tokens = (int)std::max<int64_t>(1, (T + want - 1) / want);
+    *segs = (int)std::max<int64_t>(1, (T + *tokens - 1) / *tokens);
 }
 
 }  // namespace
 
-cudaError_t launch_la_scan(const LaCore& A, cudaStream_t s, const int* only, const float* kept) {
-    if (A.B * A.H == 0) return cudaSuccess;
-    switch (A.dtype) {
-        case CT_F32: return launch_t<float>(A, s, only, kept);
-        case CT_F16: return launch_t<__half>(A, s, only, kept);
-        default: return launch_t<__nv_bfloat16>(A, s, only, kept);
-    }
+size_t la_scan_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Da, int64_t Db) {
+    int segs, tokens;
+    scan_split(B * H, T, Db, &segs, &tokens);
+    return segs > 1 ? ((size_t)B * H * Da * Db * segs * sizeof(float) + 255) / 256 * 256 : 0;
+}
+
+cudaError_t launch_la_scan(const LaCore& c, void* workspace, cudaStream_t s) {
+    ScanArgs S{c, nullptr, nullptr, 0, 0, 0};
+    int segs;
+    scan_split(c.B * c.H, c.T, c.Db, &segs, &S.seg_tokens);
+    if (segs == 1) return launch(S, 1, s);
+    float* sums = static_cast<float*>(workspace);
+    S.c.out = nullptr;
+    S.c.m_in = nullptr;
+    S.c.m_out = sums;
+    S.m_out_seg = 1;
+    cudaError_t e = launch(S, segs, s);
+    if (e != cudaSuccess) return e;
+    LaChainBatch C{};
+    C.core[0] = {sums, c.m_in, c.m_out, c.m_in_t, c.reverse, c.Da, c.Db};
+    C.log_decay = c.log_decay;
+    C.lengths = c.lengths;
+    C.T = c.T;
+    C.H = c.H;
+    C.BH = (int)(c.B * c.H);
+    C.seg_tokens = S.seg_tokens;
+    C.segs = segs;
+    e = launch_la_chain(C, 1, s);
+    if (e != cudaSuccess || !c.out) return e;
+    S.c = c;
+    S.c.m_in = sums;
+    S.c.m_in_t = 0;
+    S.c.m_out = nullptr;
+    S.m_in_seg = 1;
+    S.m_out_seg = 0;
+    return launch(S, segs, s);
+}
+
+cudaError_t launch_la_scan_again(const LaCore& c, const int* flags, const float* kept, cudaStream_t s) {
+    return launch(ScanArgs{c, flags, kept, std::max(1, c.T), 0, 0}, 1, s);
 }
 
 namespace {
@@ -199,8 +305,15 @@ struct Workspace {
     }
 };
 
+// Whichever kernel the strides lead to.
+size_t workspace_of(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int dtype, int backward) {
+    size_t n = std::max(la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, backward), la_scan_workspace_bytes(B, T, H, Dk, Dv));
+    if (backward) n = std::max(n, la_scan_workspace_bytes(B, T, H, Dv, Dk));
+    return n;
+}
+
 cudaError_t launch_core(const LaCore& c, void* workspace, cudaStream_t s) {
-    return la_tc_supports(c) ? launch_la_tc(&c, 1, workspace, s) : launch_la_scan(c, s);
+    return la_tc_supports(c) ? launch_la_tc(&c, 1, workspace, s) : launch_la_scan(c, workspace, s);
 }
 
 LaCore core_of(const float* log_decay, const int32_t* lengths, int64_t B, int64_t T, int64_t H, int dtype) {
@@ -226,7 +339,7 @@ extern "C" int ct_linear_attention_workspace_bytes(int64_t B, int64_t T, int64_t
     if (!bytes) return report_error(CT_ERR_NULL, "bytes is NULL");
     int rc = check(B, T, H, Dk, Dv, dtype);
     if (rc != CT_OK) return rc;
-    *bytes = la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, backward);
+    *bytes = workspace_of(B, T, H, Dk, Dv, dtype, backward);
     return CT_OK;
 }
 
@@ -253,7 +366,7 @@ extern "C" int ct_linear_attention_forward(const void* q, const int64_t* q_strid
     c.oscale = scale;
     cudaStream_t s = (cudaStream_t)stream;
     Workspace ws;
-    rc = ws.take(workspace, workspace_bytes, la_tc_supports(c) ? la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, 0) : 0, s);
+    rc = ws.take(workspace, workspace_bytes, workspace_of(B, T, H, Dk, Dv, dtype, 0), s);
     if (rc != CT_OK) return rc;
     return done(ws.give_back(launch_core(c, ws.p, s), s), "linear attention");
 }
@@ -279,7 +392,7 @@ extern "C" int ct_linear_attention_backward(const void* q, const int64_t* q_stri
         return report_error(CT_ERR_ALIGN, "pointers must be aligned to their element size");
     cudaStream_t s = (cudaStream_t)stream;
     Workspace ws;
-    rc = ws.take(workspace, workspace_bytes, la_tc_workspace_bytes(B, T, H, Dk, Dv, dtype, 1), s);
+    rc = ws.take(workspace, workspace_bytes, workspace_of(B, T, H, Dk, Dv, dtype, 1), s);
     if (rc != CT_OK) return rc;
     // dstate_in may be dstate_out's own buffer: the walk that writes it is the
     // last to read it

@@ -39,13 +39,33 @@ struct LaCore {
     int dtype;
 };
 
+// Sequences cut into segments: the matrix before each segment from the
+// segments' own sums ([seg][B * H][Da][Db]), in place, for up to three walks of
+// one Da * Db; the last one is the walk's result (m_out, or null).
+struct LaChain {
+    float* sums;
+    const float* m_in;
+    float* m_out;
+    int m_in_t, reverse, Da, Db;
+};
+struct LaChainBatch {
+    LaChain core[3];
+    const float* log_decay;
+    const int32_t* lengths;
+    int T, H, BH, seg_tokens, segs;
+};
+cudaError_t launch_la_chain(const LaChainBatch& c, int n, cudaStream_t stream);
+
 // Sequences of at most this many tokens go token by token.
 constexpr int kLaScanTokens = 32;
 
 // Token by token on CUDA cores, the matrix in registers
-// (ct_linear_attention.cu).  With `only` ([B * H]) the heads whose flag is 0
-// are left alone but for m_out, which is copied from `kept` where given.
-cudaError_t launch_la_scan(const LaCore& c, cudaStream_t stream, const int* only = nullptr, const float* kept = nullptr);
+// (ct_linear_attention.cu); long sequences on few heads in segments.
+size_t la_scan_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Da, int64_t Db);
+cudaError_t launch_la_scan(const LaCore& c, void* workspace, cudaStream_t stream);
+// The same again for the heads whose flag ([B * H]) is not 0, in one segment;
+// of the others only m_out is written, copied from `kept` where given.
+cudaError_t launch_la_scan_again(const LaCore& c, const int* flags, const float* kept, cudaStream_t stream);
 
 // In chunks on the tensor cores (ct_linear_attention_tc.cu): 16-bit types,
 // head sizes up to 128, tensors that TMA can address.

@@ -730,22 +730,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// The matrix before each segment from the segments' own sums, in place:
-// cur <- decay^n cur + sum, element by element along the walk; the last one is
-// the walk's result.
-struct LaChain {
-    float* sums;
-    const float* m_in;
-    float* m_out;
-    int m_in_t, reverse, Da, Db;
-};
-struct LaChainBatch {
-    LaChain core[3];
-    const float* log_decay;
-    const int32_t* lengths;
-    int T, H, BH, seg_tokens, segs;
-};
-
+// cur <- decay^n cur + sum, element by element along the walk.
 __global__ void __launch_bounds__(256) la_chain(const __grid_constant__ LaChainBatch Q) {
     const LaChain& P = Q.core[blockIdx.y];
     const int64_t msize = (int64_t)P.Da * P.Db, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -864,6 +849,12 @@ size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_
     return most;
 }
 
+cudaError_t launch_la_chain(const LaChainBatch& C, int n, cudaStream_t s) {
+    const int64_t elements = (int64_t)C.BH * C.core[0].Da * C.core[0].Db;
+    la_chain<<<dim3((unsigned)((elements + 255) / 256), n), 256, 0, s>>>(C);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream_t s) {
     DeviceInfo d;
     cudaError_t e = device_info(&d);
@@ -941,8 +932,7 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
     if (segs > 1) {
         e = launch_t<true>(Q, n, one.dtype, s);
         if (e != cudaSuccess) return e;
-        la_chain<<<dim3((unsigned)((BH * msize + 255) / 256), n), 256, 0, s>>>(C);
-        e = cudaGetLastError();
+        e = launch_la_chain(C, n, s);
         if (e != cudaSuccess) return e;
         for (int i = 0; i < n; ++i) {
             Q.core[i].m_in = C.core[i].sums;
@@ -952,7 +942,7 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
     }
     if (one.out) e = launch_t<false>(Q, n, one.dtype, s);
     else if (segs == 1) e = launch_t<true>(Q, n, one.dtype, s);  // only the last matrix is asked for
-    for (int i = 0; i < n && e == cudaSuccess && flags[i]; ++i) e = launch_la_scan(cores[i], s, flags[i], kept[i]);
+    for (int i = 0; i < n && e == cudaSuccess && flags[i]; ++i) e = launch_la_scan_again(cores[i], flags[i], kept[i], s);
     return e;
 }
 
