@@ -31,30 +31,36 @@ class Checkpoint(NamedTuple):
     dtype: torch.dtype
 
 
-def _device_of(first, *others) -> torch.device:
-    """The one CUDA device of all given tensors (None skipped)."""
-    dev = first.device
+# What follows runs on the host for every call, on tensors of any size: small
+# calls take as long as it does, so it stays short.
+
+def _index_of(first, *others) -> int:
+    """The index of the one CUDA device of all given tensors (None skipped)."""
+    index = first.get_device()
+    if index < 0:
+        raise CtError(CT_ERR_PARAM, f"device tensors expected, got {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise CtError(CT_ERR_PARAM, f"tensors must share one device, got {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise CtError(CT_ERR_PARAM, f"device tensors expected, got {dev}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise CtError(CT_ERR_PARAM, f"tensors must share one device, got {first.device} and {t.device}")
+    return index
 
 
 # The current stream's handle without building a Stream object (6 us a call on
 # the GPU's host, a quarter of a small call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _call(fn, dev, stream, *args):
+def _call(fn, index, stream, *args):
     """fn(*args, stream) with the tensors' device current."""
-    index = dev.index
-    s = _raw_stream(index) if stream is None and _raw_stream is not None else _stream_handle(stream, dev)
-    if index == torch._C._cuda_getDevice():
+    if stream is None and _raw_stream is not None:
+        s = _raw_stream(index)
+    else:
+        s = _stream_handle(stream, torch.device("cuda", index))
+    if index == (_get_device() if _get_device is not None else torch.cuda.current_device()):
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, s)
     if rc:
         _check(rc)
@@ -68,9 +74,9 @@ def _rows(t: Optional[torch.Tensor], like: Optional[torch.Tensor] = None, dtype:
         raise CtError(CT_ERR_SHAPE, f"expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise CtError(CT_ERR_DTYPE, f"expected {dtype}, got {t.dtype}")
+    if t.is_contiguous() and t.dim() > 0:
+        return t.data_ptr(), t.size(-1)
     shape, strides = t.shape, t.stride()
-    if len(shape) == 2 and (strides[1] == 1 or shape[1] == 1):
-        return t.data_ptr(), strides[0]
     if not shape:
         raise CtError(CT_ERR_SHAPE, "a tensor of at least one axis is expected")
     if strides[-1] != 1 and shape[-1] > 1:
@@ -96,8 +102,13 @@ def _dense(t: Optional[torch.Tensor]):
 
 
 def _extent(t: torch.Tensor):
-    cols = t.shape[-1]
+    cols = t.size(-1)
     return (t.numel() // cols if cols else 0), cols
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _groups(cols: int, group: int) -> int:
@@ -119,9 +130,9 @@ def _activation(a) -> int:
 
 
 def _new_checkpoint(x, quant, group) -> Checkpoint:
-    return Checkpoint(torch.empty(x.shape, dtype=_CODE_DTYPE[quant], device=x.device),
-                      torch.empty(x.shape[:-1] + (_groups(x.shape[-1], group),), dtype=torch.float32, device=x.device),
-                      group, x.dtype)
+    *lead, cols = x.shape
+    return Checkpoint(torch.empty_like(x, dtype=_CODE_DTYPE[quant], memory_format=torch.contiguous_format),
+                      torch.empty((*lead, _groups(cols, group)), dtype=torch.float32, device=x.device), group, x.dtype)
 
 
 def _kept(c: Optional[Checkpoint], like: Optional[torch.Tensor] = None):
@@ -132,13 +143,23 @@ def _kept(c: Optional[Checkpoint], like: Optional[torch.Tensor] = None):
         raise CtError(CT_ERR_DTYPE, "a checkpoint has int8 or float8_e4m3fn codes and float32 scales")
     if like is not None and c.codes.shape != like.shape:
         raise CtError(CT_ERR_SHAPE, f"expected codes of shape {tuple(like.shape)}, got {tuple(c.codes.shape)}")
-    if c.scales.shape != c.codes.shape[:-1] + (_groups(c.codes.shape[-1], c.group),):
+    *lead, cols = c.codes.shape
+    if c.scales.shape != (*lead, _groups(cols, c.group)):
         raise CtError(CT_ERR_SHAPE, f"{tuple(c.scales.shape)} scales do not fit codes of shape {tuple(c.codes.shape)} "
                                     f"in groups of {c.group}")
     return _dense(c.codes), _dense(c.scales)
 
 
 # ---- norm ------------------------------------------------------------------
+
+def _check_weight(weight, x):
+    if weight is None:
+        return
+    if weight.dim() != 1 or weight.size(0) != x.size(-1):
+        raise CtError(CT_ERR_SHAPE, f"weight must be [{x.size(-1)}], got {tuple(weight.shape)}")
+    if weight.dtype != x.dtype:
+        raise CtError(CT_ERR_DTYPE, f"weight must be {x.dtype}, got {weight.dtype}")
+
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
              eps: float = 1e-6, quant: Optional[str] = None, group: int = 128, need=("y", "rstd"), stream=None):
@@ -152,18 +173,17 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     q = _quant(quant)
     px, sx = _rows(x)
     pr, sr = _rows(residual, x, x.dtype)
-    if weight is not None and (weight.shape != x.shape[-1:] or weight.dtype != x.dtype):
-        raise CtError(CT_ERR_SHAPE if weight.shape != x.shape[-1:] else CT_ERR_DTYPE,
-                      f"weight must be [{x.shape[-1]}] of {x.dtype}")
-    dev = _device_of(x, residual, weight)
+    _check_weight(weight, x)
+    index = _index_of(x, residual, weight)
     rows, cols = _extent(x)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if "y" in need else None
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if "rstd" in need else None
+    y = _like(x) if "y" in need else None
+    h = _like(x) if residual is not None else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if "rstd" in need else None
     kept = _new_checkpoint(x, q, group) if q != CT_Q_NONE else None
-    pc, ps = (kept.codes.data_ptr(), kept.scales.data_ptr()) if kept is not None else (None, None)
-    _call(lib().ct_rms_norm_forward, dev, stream, px, sx, pr, sr, _dense(weight), _dense(y), cols, _dense(h), cols,
-          _dense(rstd), pc, ps, rows, cols, eps, dtype_code(x.dtype), q, group)
+    _call(lib().ct_rms_norm_forward, index, stream, px, sx, pr, sr, _dense(weight), y.data_ptr() if y is not None else None, cols,
+          h.data_ptr() if h is not None else None, cols, rstd.data_ptr() if rstd is not None else None,
+          kept.codes.data_ptr() if kept is not None else None, kept.scales.data_ptr() if kept is not None else None, rows, cols,
+          eps, dtype_code(x.dtype), q, group)
     return y, x if residual is None else h, rstd, kept
 
 
@@ -177,22 +197,20 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, wei
     pr, sr = _rows(dresidual, h, h.dtype)
     if rstd.shape != h.shape[:-1] or rstd.dtype != torch.float32:
         raise CtError(CT_ERR_SHAPE, f"rstd must be float32 {tuple(h.shape[:-1])}")
-    if weight is not None and (weight.shape != h.shape[-1:] or weight.dtype != h.dtype):
-        raise CtError(CT_ERR_SHAPE if weight.shape != h.shape[-1:] else CT_ERR_DTYPE,
-                      f"weight must be [{h.shape[-1]}] of {h.dtype}")
-    dev = _device_of(h, dy, rstd, weight, dresidual)
+    _check_weight(weight, h)
+    index = _index_of(h, dy, rstd, weight, dresidual)
     rows, cols = _extent(h)
     code = dtype_code(h.dtype)
-    dx = torch.empty(h.shape, dtype=h.dtype, device=dev) if "dx" in need else None
+    dx = _like(h) if "dx" in need else None
     dw = ws = None
     nws = 0
     if "dw" in need and weight is not None:
-        dw = torch.empty((cols,), dtype=h.dtype, device=dev)
+        dw = torch.empty((cols,), dtype=h.dtype, device=h.device)
         n = ctypes.c_size_t(0)
         _check(lib().ct_rms_norm_backward_workspace_bytes(rows, cols, code, ctypes.byref(n)))
         nws = n.value
-        ws = torch.empty((nws,), dtype=torch.uint8, device=dev)
-    _call(lib().ct_rms_norm_backward, dev, stream, pd, sd, ph, sh, _dense(rstd), _dense(weight), pr, sr, _dense(dx),
+        ws = torch.empty((nws,), dtype=torch.uint8, device=h.device)
+    _call(lib().ct_rms_norm_backward, index, stream, pd, sd, ph, sh, _dense(rstd), _dense(weight), pr, sr, _dense(dx),
           cols, _dense(dw), _dense(ws), nws, rows, cols, code)
     return dx, dw
 
@@ -229,10 +247,10 @@ def checkpoint_store(x: torch.Tensor, quant: str = "int8", group: int = 128, str
     if q == CT_Q_NONE:
         raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
     px, sx = _rows(x)
-    dev = _device_of(x)
+    index = _index_of(x)
     rows, cols = _extent(x)
     c = _new_checkpoint(x, q, group)
-    _call(lib().ct_checkpoint_store, dev, stream, px, sx, _dense(c.codes), _dense(c.scales), rows, cols,
+    _call(lib().ct_checkpoint_store, index, stream, px, sx, _dense(c.codes), _dense(c.scales), rows, cols,
           dtype_code(x.dtype), q, group)
     return c
 
@@ -240,10 +258,10 @@ def checkpoint_store(x: torch.Tensor, quant: str = "int8", group: int = 128, str
 def checkpoint_load(c: Checkpoint, dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, in its own dtype or another."""
     pc, ps = _kept(c)
-    dev = _device_of(c.codes, c.scales)
+    index = _index_of(c.codes, c.scales)
     rows, cols = _extent(c.codes)
-    y = torch.empty(c.codes.shape, dtype=dtype or c.dtype, device=dev)
-    _call(lib().ct_checkpoint_load, dev, stream, pc, ps, _dense(y), cols, rows, cols, dtype_code(y.dtype),
+    y = torch.empty_like(c.codes, dtype=dtype or c.dtype)
+    _call(lib().ct_checkpoint_load, index, stream, pc, ps, y.data_ptr(), cols, rows, cols, dtype_code(y.dtype),
           _QUANT_OF[c.codes.dtype], c.group)
     return y
 
@@ -257,13 +275,13 @@ def checkpointed_activation(gate: torch.Tensor, up: Optional[torch.Tensor] = Non
         raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
     pg, sg = _rows(gate)
     pu, su = _rows(up, gate, gate.dtype)
-    dev = _device_of(gate, up)
+    index = _index_of(gate, up)
     rows, cols = _extent(gate)
-    y = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+    y = _like(gate)
     cg = _new_checkpoint(gate, q, group)
     cu = _new_checkpoint(up, q, group) if up is not None else None
-    _call(lib().ct_checkpointed_activation_forward, dev, stream, pg, sg, pu, su, _dense(y), cols, _dense(cg.codes),
-          _dense(cg.scales), _dense(cu.codes) if cu else None, _dense(cu.scales) if cu else None, rows, cols, act, alpha,
+    _call(lib().ct_checkpointed_activation_forward, index, stream, pg, sg, pu, su, y.data_ptr(), cols, cg.codes.data_ptr(),
+          cg.scales.data_ptr(), cu.codes.data_ptr() if cu else None, cu.scales.data_ptr() if cu else None, rows, cols, act, alpha,
           dtype_code(gate.dtype), q, group)
     return y, cg, cu
 
@@ -280,14 +298,14 @@ def checkpointed_activation_backward(dy: Optional[torch.Tensor], gate: Checkpoin
         raise CtError(CT_ERR_PARAM, "gate and up must be kept in one format")
     dtype = dy.dtype if dy is not None else gate.dtype
     pd, sd = _rows(dy, gate.codes)
-    dev = _device_of(gate.codes, gate.scales, dy, *((up.codes, up.scales) if up is not None else ()))
+    index = _index_of(gate.codes, gate.scales, dy, *((up.codes, up.scales) if up is not None else ()))
     rows, cols = _extent(gate.codes)
 
     def new(name):
-        return torch.empty(gate.codes.shape, dtype=dtype, device=dev) if name in need else None
+        return torch.empty_like(gate.codes, dtype=dtype) if name in need else None
 
     dgate, dup, y = new("dgate"), new("dup") if up is not None else None, new("y")
-    _call(lib().ct_checkpointed_activation_backward, dev, stream, pd, sd, pg, sg, pu, su, _dense(dgate), cols,
+    _call(lib().ct_checkpointed_activation_backward, index, stream, pd, sd, pg, sg, pu, su, _dense(dgate), cols,
           _dense(dup), cols, _dense(y), cols, rows, cols, act, alpha, dtype_code(dtype), _QUANT_OF[gate.codes.dtype],
           gate.group)
     return (dgate, dup, y) if "y" in need else (dgate, dup)
@@ -378,13 +396,14 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     pq, sq = _heads(q, (B, T, H, Dk), dt)
     pk, sk = _heads(k, (B, T, H, Dk), dt)
     pv, sv = _heads(v, (B, T, H, Dv), dt)
-    dev = _device_of(q, k, v, log_decay, state, lengths, state_out)
+    index = _index_of(q, k, v, log_decay, state, lengths, state_out)
+    dev = q.device
     o = torch.empty((B, T, H, Dv), dtype=dt, device=dev)
     if state_out is None and "state" in need:
         state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     code = dtype_code(dt)
     ws, nws = _attention_workspace(B, T, H, Dk, Dv, code, 0, dev)
-    _call(lib().ct_linear_attention_forward, dev, stream, pq, sq, pk, sk, pv, sv, _dense(o),
+    _call(lib().ct_linear_attention_forward, index, stream, pq, sq, pk, sk, pv, sv, _dense(o),
           _I64x3(T * H * Dv, H * Dv, Dv), _dense(log_decay), _dense(state), _dense(state_out), _dense(lengths),
           _dense(ws), nws, B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
     return o, state_out
@@ -401,7 +420,8 @@ def linear_attention_backward(q, k, v, log_decay, do, state=None, dstate=None, l
     pk, sk = _heads(k, (B, T, H, Dk), dt)
     pv, sv = _heads(v, (B, T, H, Dv), dt)
     po, so = _heads(do, (B, T, H, Dv), dt)
-    dev = _device_of(q, k, v, log_decay, do, state, dstate, lengths)
+    index = _index_of(q, k, v, log_decay, do, state, dstate, lengths)
+    dev = q.device
 
     def new(name, D):
         return torch.empty((B, T, H, D), dtype=dt, device=dev) if name in need else None
@@ -413,7 +433,7 @@ def linear_attention_backward(q, k, v, log_decay, do, state=None, dstate=None, l
     sqk, svv = _I64x3(T * H * Dk, H * Dk, Dk), _I64x3(T * H * Dv, H * Dv, Dv)
     code = dtype_code(dt)
     ws, nws = _attention_workspace(B, T, H, Dk, Dv, code, 1, dev)
-    _call(lib().ct_linear_attention_backward, dev, stream, pq, sq, pk, sk, pv, sv, po, so, _dense(log_decay),
+    _call(lib().ct_linear_attention_backward, index, stream, pq, sq, pk, sk, pv, sv, po, so, _dense(log_decay),
           _dense(state), _dense(dstate), _dense(lengths), _dense(dq), sqk, _dense(dk), sqk, _dense(dv), svv,
           _dense(dfirst), _dense(ws), nws, B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
     return dq, dk, dv, dfirst

@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(const __grid_constant__ S
     const LaCore& A = S.c;
     constexpr int D = kWarps * 4 * RX, kThreads = kWarps * 32;  // D: rows held (>= Da)
     constexpr int NX = TB * D / kThreads, NY = TB * kCols / kThreads;
+    static_assert(NX > 0 && NY > 0, "a thread stages whole elements");
     __shared__ __align__(16) float xs[TB][D];
     __shared__ __align__(16) float zs[TB][D];
     __shared__ __align__(16) float ys[TB][kCols];
@@ -92,8 +93,10 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(const __grid_constant__ S
     // result after 300 tokens.  So the first step of every further round of TB
     // takes what makes the round's product exp(TB g).
     if (tid == 0 && n > TB) {
-        const double e = gamma, e2 = e * e, e4 = e2 * e2, e7 = e4 * e2 * e;
-        first_gamma = gamma > 1e-10f ? (float)(exp((double)TB * (double)A.log_decay[h]) / (TB == 16 ? e7 * e4 * e4 : e7)) : gamma;
+        double p = 1.0;
+#pragma unroll 1
+        for (int i = 1; i < TB; ++i) p *= (double)gamma;
+        first_gamma = gamma > 1e-10f ? (float)(exp((double)TB * (double)A.log_decay[h]) / p) : gamma;
     }
     float px[NX], pz[NX], py[NY];
     auto fetch = [&](int t0) {
@@ -186,15 +189,22 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(const __grid_constant__ S
     }
 }
 
-template <typename T>
-cudaError_t launch_t(const ScanArgs& S, int segs, cudaStream_t s) {
+template <typename T, int TB>
+cudaError_t launch_tb(const ScanArgs& S, int segs, cudaStream_t s) {
     const LaCore& A = S.c;
     const dim3 grid((unsigned)(A.B * A.H), (unsigned)((A.Db + kCols - 1) / kCols), (unsigned)segs);
-    if (A.Da <= 32) la_scan<T, 2, 16><<<grid, kWarps * 32, 0, s>>>(S);
-    else if (A.Da <= 64) la_scan<T, 4, 16><<<grid, kWarps * 32, 0, s>>>(S);
-    else if (A.Da <= 128) la_scan<T, 8, 16><<<grid, kWarps * 32, 0, s>>>(S);
-    else la_scan<T, 16, 8><<<grid, kWarps * 32, 0, s>>>(S);
+    if (A.Da <= 32) la_scan<T, 2, TB><<<grid, kWarps * 32, 0, s>>>(S);
+    else if (A.Da <= 64) la_scan<T, 4, TB><<<grid, kWarps * 32, 0, s>>>(S);
+    else if (A.Da <= 128) la_scan<T, 8, TB><<<grid, kWarps * 32, 0, s>>>(S);
+    else la_scan<T, 16, TB < 8 ? TB : 8><<<grid, kWarps * 32, 0, s>>>(S);
     return cudaGetLastError();
+}
+
+// Streaming steps stage four tokens: fewer registers, so more of the state in
+// flight (64 x 8 heads of 128 x 128: 26 us with sixteen).
+template <typename T>
+cudaError_t launch_t(const ScanArgs& S, int segs, cudaStream_t s) {
+    return S.c.T <= 4 ? launch_tb<T, 4>(S, segs, s) : launch_tb<T, 16>(S, segs, s);
 }
 
 cudaError_t launch(const ScanArgs& S, int segs, cudaStream_t s) {
