@@ -185,3 +185,23 @@ def test_autograd_against_differences():
         assert abs(terms.sum().item() - want) <= 300 * E * terms.abs().sum().item() + 1e-6
     y1 = ct.rms_norm_autograd(leaves[0], leaves[1])
     assert y1.grad_fn is not None and torch.equal(y1, ct.rms_norm(x, w)[0])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [64, 256, 264, 1000, 2048, 2944])
+def test_forward_of_many_rows(cols, dtype):
+    """Enough rows that the blocks walk them: every row right, h over the residual, reproducible."""
+    rows = 45001 if cols < 512 else 21000 if cols <= 1000 else 9001
+    g = gen(cols)
+    x, r, w = randn(g, rows, cols, dtype=dtype), randn(g, rows, cols, dtype=dtype), randn(g, cols, dtype=dtype)
+    y, h, rstd, kept = ct.rms_norm(x, w, r, quant="int8", group=64)
+    exact = check_norm(x, w, r, 1e-6, dtype, y, h, rstd)
+    scale = kept.scales.double().repeat_interleave(64, 1)[:, :cols]
+    within(decoded(kept), exact, scale * 0.50005 + exact.abs() * 4 * norm_chain(cols) * E, "8-bit y")
+    del exact, scale
+    stream, y2 = r.clone(), torch.empty_like(x)
+    rc = ct.lib().ct_rms_norm_forward(x.data_ptr(), cols, stream.data_ptr(), cols, w.data_ptr(), y2.data_ptr(), cols, stream.data_ptr(),
+                                      cols, None, None, None, rows, cols, 1e-6, ct.dtype_code(x.dtype), 0, 128,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == ct.CT_OK and torch.equal(stream, h) and torch.equal(y2, y)
+    assert torch.equal(ct.rms_norm(x, None, None)[0], ct.rms_norm(x, None, None)[0])

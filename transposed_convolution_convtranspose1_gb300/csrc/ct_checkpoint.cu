@@ -26,7 +26,7 @@ struct ActFwd {
     float *gsc, *usc;
     int64_t gs, us, ys;
     int64_t rows;
-    int cols, group, n_groups;
+    int cols, group, group_shift, n_groups;
     float alpha;
 };
 
@@ -37,7 +37,7 @@ struct ActBwd {
     void *dgate, *dup, *y;
     int64_t dys, dgs, dus, ys;
     int64_t rows;
-    int cols, group, n_groups;
+    int cols, group, group_shift, n_groups;
     float alpha;
 };
 
@@ -85,9 +85,10 @@ __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P, Pieces W) {
         if (in[j] && P.y) {
             float o[VEC];
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                o[k] = act_value<A, sizeof(T) == 2>(a[k], P.alpha);
-                if (P.up) o[k] *= b[k];
+            for (int k = 0; k < VEC; k += 2) {
+                float2 f = act_value2<A, sizeof(T) == 2>(pair(a + k), P.alpha);
+                if (P.up) f = __fmul2_rn(f, pair(b + k));
+                put(o + k, f);
             }
             Vec<T, VEC> ov;
             ov.set(o);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_vec(ActFwd P, Pieces W) {
         }
         if (!in[j]) continue;
         const bool first = (threadIdx.x & (lanes - 1)) == 0;
-        const int64_t at = row[j] * P.n_groups + col[j] / P.group;
+        const int64_t at = row[j] * P.n_groups + (col[j] >> P.group_shift);
         float scale, inv;
         group_scale<Q>(Vec<T, VEC>::to_abs_bits(amax), scale, inv);
         store_codes<Q, VEC>(P.gc + row[j] * P.cols + col[j], a, inv);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P, Pieces W) {
         in[j] = i < W.n;
         usc[j] = 1.f;
         if (in[j]) {
-            const int64_t at = row[j] * P.n_groups + col[j] / P.group;
+            const int64_t at = row[j] * P.n_groups + (col[j] >> P.group_shift);
             if (P.dy) dv[j].load(static_cast<const T*>(P.dy) + row[j] * P.dys + col[j]);
             code_words<VEC>(P.gc + row[j] * P.cols + col[j], gw[j]);
             if (P.uc) code_words<VEC>(P.uc + row[j] * P.cols + col[j], uw[j]);
@@ -156,29 +157,33 @@ __global__ void __launch_bounds__(kThreads) act_bwd_vec(ActBwd P, Pieces W) {
             if (P.uc) decode4<Q>(uw[j][k], b + 4 * k);
         }
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            a[k] *= gsc[j];
-            if (P.uc) b[k] *= usc[j];
-            act_both<A, sizeof(T) == 2>(a[k], P.alpha, f[k], slope[k]);
+        for (int k = 0; k < VEC; k += 2) {
+            put(a + k, __fmul2_rn(pair(a + k), twice(gsc[j])));
+            if (P.uc) put(b + k, __fmul2_rn(pair(b + k), twice(usc[j])));
+            float2 f2, s2;
+            act_both2<A, sizeof(T) == 2>(pair(a + k), P.alpha, f2, s2);
+            put(f + k, f2);
+            put(slope + k, s2);
         }
         if (P.y) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) o[k] = P.uc ? f[k] * b[k] : f[k];
+            for (int k = 0; k < VEC; k += 2) put(o + k, P.uc ? __fmul2_rn(pair(f + k), pair(b + k)) : pair(f + k));
             ov.set(o);
             ov.store(static_cast<T*>(P.y) + row[j] * P.ys + col[j]);
         }
         if (P.dgate) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                o[k] = dv[j].get(k) * slope[k];
-                if (P.uc) o[k] *= b[k];
+            for (int k = 0; k < VEC; k += 2) {
+                float2 d = __fmul2_rn(make_float2(dv[j].get(k), dv[j].get(k + 1)), pair(slope + k));
+                if (P.uc) d = __fmul2_rn(d, pair(b + k));
+                put(o + k, d);
             }
             ov.set(o);
             ov.store(static_cast<T*>(P.dgate) + row[j] * P.dgs + col[j]);
         }
         if (P.dup) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) o[k] = dv[j].get(k) * f[k];
+            for (int k = 0; k < VEC; k += 2) put(o + k, __fmul2_rn(make_float2(dv[j].get(k), dv[j].get(k + 1)), pair(f + k)));
             ov.set(o);
             ov.store(static_cast<T*>(P.dup) + row[j] * P.dus + col[j]);
         }
@@ -199,8 +204,8 @@ __device__ __forceinline__ void slot_max(unsigned (&m)[4], int group) {
 
 // Codes and scales of a warp's 128 values (n of them inside the row).
 template <int Q>
-__device__ __forceinline__ void keep(const float (&v)[4], const unsigned (&m)[4], int n, int lane, int group, uint8_t* codes,
-                                     float* scales) {
+__device__ __forceinline__ void keep(const float (&v)[4], const unsigned (&m)[4], int n, int lane, int group, int shift,
+                                     uint8_t* codes, float* scales) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int k = j * 32 + lane;
@@ -208,7 +213,7 @@ __device__ __forceinline__ void keep(const float (&v)[4], const unsigned (&m)[4]
         group_scale<Q>(m[j], scale, inv);
         if (k < n) {
             codes[k] = encode<Q>(v[j], inv);
-            if (k % group == 0) scales[k / group] = scale;
+            if ((k & (group - 1)) == 0) scales[k >> shift] = scale;
         }
     }
 }
@@ -245,12 +250,12 @@ __global__ void __launch_bounds__(kThreads) act_fwd_any(ActFwd P, Pieces W) {
             y[k] = from_f32<T>(u ? v * b[j] : v);
         }
     }
-    const int64_t at = row * P.n_groups + c0 / P.group;
+    const int64_t at = row * P.n_groups + (c0 >> P.group_shift);
     slot_max(amax, P.group);
-    keep<Q>(a, amax, n, lane, P.group, P.gc + row * P.cols + c0, P.gsc + at);
+    keep<Q>(a, amax, n, lane, P.group, P.group_shift, P.gc + row * P.cols + c0, P.gsc + at);
     if (u) {
         slot_max(bmax, P.group);
-        keep<Q>(b, bmax, n, lane, P.group, P.uc + row * P.cols + c0, P.usc + at);
+        keep<Q>(b, bmax, n, lane, P.group, P.group_shift, P.uc + row * P.cols + c0, P.usc + at);
     }
 }
 
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_any(ActBwd P, Pieces W) {
     unsigned piece;
     const unsigned r32 = divide(i, W.per_row, &piece);
     const int c0 = (int)piece * 128, n = min(128, P.cols - c0);
-    const int64_t row = r32, at = row * P.n_groups + c0 / P.group;
+    const int64_t row = r32, at = row * P.n_groups + (c0 >> P.group_shift);
     const uint8_t* gc = P.gc + row * P.cols + c0;
     const uint8_t* uc = P.uc ? P.uc + row * P.cols + c0 : nullptr;
     const T* dy = P.dy ? static_cast<const T*>(P.dy) + row * P.dys + c0 : nullptr;
@@ -272,8 +277,8 @@ __global__ void __launch_bounds__(kThreads) act_bwd_any(ActBwd P, Pieces W) {
     for (int j = 0; j < 4; ++j) {
         const int k = j * 32 + lane;
         const bool in = k < n;
-        a[j] = in ? decode<Q>(gc[k]) * P.gsc[at + k / P.group] : 0.f;
-        b[j] = uc && in ? decode<Q>(uc[k]) * P.usc[at + k / P.group] : 1.f;
+        a[j] = in ? decode<Q>(gc[k]) * P.gsc[at + (k >> P.group_shift)] : 0.f;
+        b[j] = uc && in ? decode<Q>(uc[k]) * P.usc[at + (k >> P.group_shift)] : 1.f;
         d[j] = dy && in ? to_f32(dy[k]) : 0.f;
     }
 #pragma unroll
@@ -389,6 +394,8 @@ cudaError_t run_bwd(const ActBwd& P, int act, int dtype, int quant, cudaStream_t
     }
 }
 
+int shift_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+
 bool bad_ptr(const void* p, size_t a) { return p && (uintptr_t)p % a != 0; }
 
 int check(int64_t rows, int64_t cols, int activation, int dtype, int quant, int group) {
@@ -428,7 +435,7 @@ extern "C" int ct_checkpointed_activation_forward(const void* gate, int64_t gate
     if (bad_ptr(gate, eb) || bad_ptr(up, eb) || bad_ptr(y, eb) || bad_ptr(gate_scales, 4) || bad_ptr(up_scales, 4))
         return report_error(CT_ERR_ALIGN, "pointers must be aligned to their element size");
     ActFwd P{gate, up, y, static_cast<uint8_t*>(gate_codes), static_cast<uint8_t*>(up_codes), gate_scales, up_scales,
-             gate_stride, up_stride, y_stride, rows, (int)cols, group, (int)((cols + group - 1) / group), alpha};
+             gate_stride, up_stride, y_stride, rows, (int)cols, group, shift_of(group), (int)((cols + group - 1) / group), alpha};
     return done(run_fwd(P, activation, dtype, quant, (cudaStream_t)stream), "checkpointed activation");
 }
 
@@ -449,7 +456,7 @@ extern "C" int ct_checkpointed_activation_backward(const void* dy, int64_t dy_st
     if (!dgate && !dup && !y) return CT_OK;
     ActBwd P{dgate || dup ? dy : nullptr, static_cast<const uint8_t*>(gate_codes), static_cast<const uint8_t*>(up_codes),
              gate_scales, up_scales, dgate, dup, y, dy_stride, dgate_stride, dup_stride, y_stride, rows, (int)cols, group,
-             (int)((cols + group - 1) / group), alpha};
+             shift_of(group), (int)((cols + group - 1) / group), alpha};
     return done(run_bwd(P, activation, dtype, quant, (cudaStream_t)stream), "checkpointed activation backward");
 }
 

@@ -230,20 +230,11 @@ template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
 template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// v = hi + lo to within U^2 |v|, each half a T.  bf16 takes the upper half of
-// the fp32 word as it is (no conversion instruction); lo has the rest.
+// v = hi + lo to within U^2 |v|, each half a T.
 template <typename T>
 __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
-    float2 h;
-    if constexpr (std::is_same<T, __half>::value) {
-        hi = pack2<T>(v.x, v.y);
-        h = unpack2<T>(hi);
-    } else {
-        const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
-        hi = __byte_perm(a, b, 0x7632);
-        h = make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u));
-    }
-    const float2 r = __ffma2_rn(h, make_float2(-1.f, -1.f), v);
+    hi = pack2<T>(v.x, v.y);
+    const float2 r = __ffma2_rn(unpack2<T>(hi), make_float2(-1.f, -1.f), v);
     lo = pack2<T>(r.x, r.y);
 }
 

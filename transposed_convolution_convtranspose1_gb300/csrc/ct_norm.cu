@@ -30,7 +30,7 @@ struct NormFwd {
     float* scales;
     int64_t xs, rs, ys, hs;  // row strides, elements
     int64_t rows;
-    int cols, group, quant;
+    int cols, group, group_shift, quant;
     float eps;
 };
 
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_rows(NormFwd A) {
         T* y = A.y ? static_cast<T*>(A.y) + row * A.ys : nullptr;
         T* h = A.h ? static_cast<T*>(A.h) + row * A.hs : nullptr;
         const int lane = threadIdx.x & 31;
-        const int n_groups = (A.cols + A.group - 1) / A.group;
+        const int n_groups = (A.cols + A.group - 1) >> A.group_shift;
         for (int g = threadIdx.x >> 5; g < n_groups; g += kThreads / 32) {
             float v[4];
             unsigned amax = 0;
@@ -131,18 +131,30 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_regs(NormFwd A) {
         }
     }
     float s[NV][VEC], ss = 0.f;
+    if constexpr (VEC > 1) {
+        float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            s[v][i] = xv[v].get(i) + rv[v].get(i);  // + 0 without a residual: only a zero's sign can change
-            ss = fmaf(s[v][i], s[v][i], ss);
+            for (int i = 0; i < VEC; i += 2) {
+                // + 0 without a residual: only a zero's sign can change
+                const float2 p = __fadd2_rn(make_float2(xv[v].get(i), xv[v].get(i + 1)), make_float2(rv[v].get(i), rv[v].get(i + 1)));
+                put(s[v] + i, p);
+                sq = __ffma2_rn(p, p, sq);
+            }
+        ss = sq.x + sq.y;
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            s[v][0] = xv[v].get(0) + rv[v].get(0);
+            ss = fmaf(s[v][0], s[v][0], ss);
         }
+    }
     if constexpr (TPR == 32) ss = warp_sum(ss);
     else ss = block_sum<THREADS>(ss, part);
     const float rstd = 1.f / sqrtf(ss / (float)A.cols + A.eps);
     if (tid == 0 && A.rstd) A.rstd[row] = rstd;
-    const int n_groups = (A.cols + A.group - 1) / A.group;
+    const int n_groups = (A.cols + A.group - 1) >> A.group_shift;
     [[maybe_unused]] unsigned amax1[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -154,10 +166,17 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_regs(NormFwd A) {
                 o.set(s[v]);
                 o.store(static_cast<T*>(A.h) + row * A.hs + col[v]);
             }
+            if constexpr (VEC > 1) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                y[i] = s[v][i] * rstd * (w ? wv[v].get(i) : 1.f);
-                top = abs_max(top, y[i]);
+                for (int i = 0; i < VEC; i += 2) {
+                    float2 p = __fmul2_rn(pair(s[v] + i), twice(rstd));
+                    if (w) p = __fmul2_rn(p, make_float2(wv[v].get(i), wv[v].get(i + 1)));
+                    put(y + i, p);
+                    top = abs_max(top, p.x, p.y);
+                }
+            } else {
+                y[0] = s[v][0] * rstd * (w ? wv[v].get(0) : 1.f);
+                top = fabsf(y[0]);
             }
             if (A.y) {
                 Vec<T, VEC> o;
@@ -168,7 +187,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_regs(NormFwd A) {
         if (A.quant == CT_Q_NONE) continue;
         unsigned amax = abs_bits(top);
         if constexpr (VEC > 1) {
-            const int lanes = A.group / VEC;
+            const int lanes = A.group / VEC;  // VEC is a power of two
             amax = lanes_max(amax, lanes);
             float scale, inv;
             if (A.quant == CT_Q_INT8) group_scale<CT_Q_INT8>(amax, scale, inv);
@@ -177,7 +196,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_regs(NormFwd A) {
                 uint8_t* c = A.codes + row * A.cols + col[v];
                 if (A.quant == CT_Q_INT8) store_codes<CT_Q_INT8, VEC>(c, y, inv);
                 else store_codes<CT_Q_E4M3, VEC>(c, y, inv);
-                if ((lane & (lanes - 1)) == 0) A.scales[row * n_groups + col[v] / A.group] = scale;
+                if ((lane & (lanes - 1)) == 0) A.scales[row * n_groups + (col[v] >> A.group_shift)] = scale;
             }
         } else {
             amax1[v] = __reduce_max_sync(0xffffffffu, amax);
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_regs(NormFwd A) {
                 if (A.quant == CT_Q_INT8) group_scale<CT_Q_INT8>(amax, scale, inv);
                 else group_scale<CT_Q_E4M3>(amax, scale, inv);
                 A.codes[row * A.cols + col[v]] = A.quant == CT_Q_INT8 ? encode<CT_Q_INT8>(s[v][0], inv) : encode<CT_Q_E4M3>(s[v][0], inv);
-                if (col[v] % A.group == 0) A.scales[row * n_groups + col[v] / A.group] = scale;
+                if ((col[v] & (A.group - 1)) == 0) A.scales[row * n_groups + (col[v] >> A.group_shift)] = scale;
             }
         }
     }
@@ -608,7 +627,7 @@ extern "C" int ct_rms_norm_forward(const void* x, int64_t x_stride, const void* 
         bad_ptr(rstd, 4) || bad_ptr(scales, 4))
         return report_error(CT_ERR_ALIGN, "pointers must be aligned to their element size");
     NormFwd A{x, residual, weight, y, h, rstd, static_cast<uint8_t*>(codes), scales, x_stride, residual_stride,
-              y_stride, h_stride, rows, (int)cols, quant != CT_Q_NONE ? group : 128, quant, eps};
+              y_stride, h_stride, rows, (int)cols, quant != CT_Q_NONE ? group : 128, group == 32 ? 5 : group == 64 ? 6 : 7, quant, eps};
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = dtype == CT_F32 ? launch_fwd<float>(A, s) : dtype == CT_F16 ? launch_fwd<__half>(A, s)
                                                                               : launch_fwd<__nv_bfloat16>(A, s);

@@ -33,12 +33,21 @@ constexpr float kMinNormal = 1.17549435e-38f;
 // whether anything is not finite (fmaxf would drop a NaN).
 __device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// max(a, |v|) that keeps a NaN once it has met one.
-__device__ __forceinline__ float abs_max(float a, float v) {
+// max(a, |v|, |w|) that keeps a NaN once it has met one.
+__device__ __forceinline__ float abs_max(float a, float v, float w) {
     float m;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(v)));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(fabsf(v)), "f"(fabsf(w)));
     return m;
 }
+// Two adjacent values of an array as the operand of a packed instruction
+// (one issue for two fp32 operations, each rounded as usual): the kernels
+// here are bound by instruction issue before they are bound by memory.
+__device__ __forceinline__ float2 pair(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ void put(float* v, float2 p) {
+    v[0] = p.x;
+    v[1] = p.y;
+}
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
 // Scale and reciprocal scale of a group from the maximum of its abs_bits.
 // Q: CT_Q_INT8 or CT_Q_E4M3.  inv = 0 marks a group whose codes are all 0.
@@ -58,8 +67,9 @@ __device__ __forceinline__ void group_scale(unsigned amax_bits, float& scale, fl
 // instructions run at an eighth of the add's rate, and two for each element
 // were what bounded the activation's forward pass (16384 x 4096 gated bf16:
 // 146 us with them).
+constexpr float kIntBits = 12582912.f;
 __device__ __forceinline__ uint32_t int_bits(float v, float inv) {
-    return __float_as_uint(__fadd_rn(__fmul_rn(v, inv), 12582912.f));
+    return __float_as_uint(__fadd_rn(__fmul_rn(v, inv), kIntBits));
 }
 
 // Four codes in one word; inv = 0 gives codes 0 whatever v is (infinity * 0
@@ -67,14 +77,15 @@ __device__ __forceinline__ uint32_t int_bits(float v, float inv) {
 template <int Q>
 __device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
     uint32_t c;
+    const float2 a = __fmul2_rn(pair(v), twice(inv)), b = __fmul2_rn(pair(v + 2), twice(inv));
     if constexpr (Q == CT_Q_INT8) {
-        const uint32_t lo = __byte_perm(int_bits(v[0], inv), int_bits(v[1], inv), 0x0040);
-        const uint32_t hi = __byte_perm(int_bits(v[2], inv), int_bits(v[3], inv), 0x0040);
+        // single additions: a packed one would be fused with the packed product
+        const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a.x, kIntBits)), __float_as_uint(__fadd_rn(a.y, kIntBits)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(b.x, kIntBits)), __float_as_uint(__fadd_rn(b.y, kIntBits)), 0x0040);
         c = __byte_perm(lo, hi, 0x5410);
     } else {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
-        c = lo | hi << 16;
+        c = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+            (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
     }
     return inv == 0.f ? 0u : c;
 }
@@ -136,6 +147,29 @@ __device__ __forceinline__ float act_value(float v, float alpha) {
     else return act_fixed<A>(v, alpha);
 }
 
+// Two at a time.
+template <bool FAST>
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    if constexpr (FAST) {
+        const float2 t = __fmul2_rn(v, twice(-1.4426950408889634f));
+        float2 e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+        e = __fadd2_rn(e, twice(1.f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+        return r;
+    } else {
+        return make_float2(sigmoid<false>(v.x), sigmoid<false>(v.y));
+    }
+}
+template <int A, bool FAST>
+__device__ __forceinline__ float2 act_value2(float2 v, float alpha) {
+    if constexpr (A == 3) return __fmul2_rn(v, sigmoid2<FAST>(v));
+    else if constexpr (A == 6) return sigmoid2<FAST>(v);
+    else return make_float2(act_value<A, FAST>(v.x, alpha), act_value<A, FAST>(v.y, alpha));
+}
+
 template <int A, bool FAST>
 __device__ __forceinline__ void act_both(float v, float alpha, float& f, float& slope) {
     if constexpr (A == 1) {
@@ -161,6 +195,18 @@ __device__ __forceinline__ void act_both(float v, float alpha, float& f, float& 
     } else {
         f = v;
         slope = 1.f;
+    }
+}
+
+template <int A, bool FAST>
+__device__ __forceinline__ void act_both2(float2 v, float alpha, float2& f, float2& slope) {
+    if constexpr (A == 3) {
+        const float2 s = sigmoid2<FAST>(v);
+        f = __fmul2_rn(v, s);
+        slope = __ffma2_rn(f, __ffma2_rn(s, twice(-1.f), twice(1.f)), s);
+    } else {
+        act_both<A, FAST>(v.x, alpha, f.x, slope.x);
+        act_both<A, FAST>(v.y, alpha, f.y, slope.y);
     }
 }
 
@@ -287,13 +333,17 @@ __device__ __forceinline__ unsigned divide(unsigned i, Divider v, unsigned* rest
 
 // Both halves of a word reduced at once (two 16-bit maxima in one).
 __device__ __forceinline__ uint32_t lanes_max2(uint32_t v, int lanes) {
-    for (int o = lanes >> 1; o; o >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o < lanes) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
 // Maximum over `lanes` (a power of two) neighbouring lanes.
 __device__ __forceinline__ unsigned lanes_max(unsigned v, int lanes) {
-    for (int o = lanes >> 1; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        if (o < lanes) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
