@@ -70,13 +70,14 @@ def _rows(t: Optional[torch.Tensor], like: Optional[torch.Tensor] = None, dtype:
     """(pointer, row stride) of a tensor read as a matrix of its last axis."""
     if t is None:
         return None, 0
-    if like is not None and t.shape != like.shape:
-        raise CtError(CT_ERR_SHAPE, f"expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    shape = t.shape
+    if like is not None and shape != like.shape:
+        raise CtError(CT_ERR_SHAPE, f"expected shape {tuple(like.shape)}, got {tuple(shape)}")
+    if dtype is not None and t.dtype is not dtype:
         raise CtError(CT_ERR_DTYPE, f"expected {dtype}, got {t.dtype}")
-    if t.is_contiguous() and t.dim() > 0:
-        return t.data_ptr(), t.size(-1)
-    shape, strides = t.shape, t.stride()
+    if shape and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    strides = t.stride()
     if not shape:
         raise CtError(CT_ERR_SHAPE, "a tensor of at least one axis is expected")
     if strides[-1] != 1 and shape[-1] > 1:
@@ -102,13 +103,16 @@ def _dense(t: Optional[torch.Tensor]):
 
 
 def _extent(t: torch.Tensor):
-    cols = t.size(-1)
+    shape = t.shape
+    if len(shape) == 2:
+        return shape
+    cols = shape[-1]
     return (t.numel() // cols if cols else 0), cols
 
 
 def _like(t: torch.Tensor) -> torch.Tensor:
     """A new dense tensor of t's shape and type."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _groups(cols: int, group: int) -> int:
@@ -130,9 +134,11 @@ def _activation(a) -> int:
 
 
 def _new_checkpoint(x, quant, group) -> Checkpoint:
-    *lead, cols = x.shape
-    return Checkpoint(torch.empty_like(x, dtype=_CODE_DTYPE[quant], memory_format=torch.contiguous_format),
-                      torch.empty((*lead, _groups(cols, group)), dtype=torch.float32, device=x.device), group, x.dtype)
+    shape = x.shape
+    codes = torch.empty(shape, dtype=_CODE_DTYPE[quant], device=x.device)
+    n = _groups(shape[-1], group)
+    scales = torch.empty((shape[0], n) if len(shape) == 2 else (*shape[:-1], n), dtype=torch.float32, device=x.device)
+    return Checkpoint(codes, scales, group, x.dtype)
 
 
 def _kept(c: Optional[Checkpoint], like: Optional[torch.Tensor] = None):
@@ -143,8 +149,8 @@ def _kept(c: Optional[Checkpoint], like: Optional[torch.Tensor] = None):
         raise CtError(CT_ERR_DTYPE, "a checkpoint has int8 or float8_e4m3fn codes and float32 scales")
     if like is not None and c.codes.shape != like.shape:
         raise CtError(CT_ERR_SHAPE, f"expected codes of shape {tuple(like.shape)}, got {tuple(c.codes.shape)}")
-    *lead, cols = c.codes.shape
-    if c.scales.shape != (*lead, _groups(cols, c.group)):
+    shape = c.codes.shape
+    if c.scales.shape != (*shape[:-1], _groups(shape[-1], c.group)):
         raise CtError(CT_ERR_SHAPE, f"{tuple(c.scales.shape)} scales do not fit codes of shape {tuple(c.codes.shape)} "
                                     f"in groups of {c.group}")
     return _dense(c.codes), _dense(c.scales)
@@ -155,9 +161,9 @@ def _kept(c: Optional[Checkpoint], like: Optional[torch.Tensor] = None):
 def _check_weight(weight, x):
     if weight is None:
         return
-    if weight.dim() != 1 or weight.size(0) != x.size(-1):
+    if weight.shape != x.shape[-1:]:
         raise CtError(CT_ERR_SHAPE, f"weight must be [{x.size(-1)}], got {tuple(weight.shape)}")
-    if weight.dtype != x.dtype:
+    if weight.dtype is not x.dtype:
         raise CtError(CT_ERR_DTYPE, f"weight must be {x.dtype}, got {weight.dtype}")
 
 
@@ -178,7 +184,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     rows, cols = _extent(x)
     y = _like(x) if "y" in need else None
     h = _like(x) if residual is not None else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if "rstd" in need else None
+    rstd = torch.empty(rows if x.dim() == 2 else x.shape[:-1], dtype=torch.float32, device=x.device) if "rstd" in need else None
     kept = _new_checkpoint(x, q, group) if q != CT_Q_NONE else None
     _call(lib().ct_rms_norm_forward, index, stream, px, sx, pr, sr, _dense(weight), y.data_ptr() if y is not None else None, cols,
           h.data_ptr() if h is not None else None, cols, rstd.data_ptr() if rstd is not None else None,
