@@ -85,11 +85,21 @@ struct LaTcBatch {
 };
 
 // Tile n of the walk (Z, X, Y of chunk 0, Z, X, Y of chunk 1, ...) lies in
-// place n % 5 of the ring; M's hi and lo parts after it.
+// place n % 5 of the ring; M's parts after it, and decayed x where it is an
+// operand in shared memory.
+//
+// kStacked (64 x 64): x enters as its hi and lo parts one above the other, 128
+// rows of one MMA, and so does M: its first 64 TMEM rows sum the hi products,
+// the last 64 the lo products, and Z M takes hi and lo of the first and hi of
+// the second.  Against x in TMEM, 64 of whose 128 rows are empty at this size,
+// the new M takes half the MMAs, and all lanes and warps share the work.
 template <int DA, int DB>
 struct LaShape {
+    static constexpr bool kStacked = DA == 64 && DB == 64;
     static constexpr uint32_t kTile = 256 * (DA > DB ? DA : DB), kM = 2 * DA * DB;
-    static constexpr uint32_t oM = 5 * kTile, kBytes = oM + 2 * kM;
+    static constexpr int kMParts = kStacked ? 3 : 2;
+    static constexpr uint32_t oM = 5 * kTile, oX = oM + kMParts * kM, kX = kStacked ? 32768 : 0;
+    static constexpr uint32_t kBytes = oX + 2 * kX;
     static __device__ __forceinline__ uint32_t z(int c) { return (uint32_t)(3 * c % 5) * kTile; }
     static __device__ __forceinline__ uint32_t x(int c) { return (uint32_t)((3 * c + 1) % 5) * kTile; }
     static __device__ __forceinline__ uint32_t y(int c) { return (uint32_t)((3 * c + 2) % 5) * kTile; }
@@ -211,6 +221,9 @@ __device__ __forceinline__ void tmem_st_scaled(uint32_t taddr, const float* v, f
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Two fp32 values as one word of two T.
@@ -257,13 +270,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // them the flag has the head done again
     constexpr float kUp = kHalf ? 16.f : 1.f, kUpX = kHalf ? 64.f : 1.f;
     constexpr int kN = DB / 4;  // columns of Y, M and out a warp has
+    constexpr bool kStacked = Sh::kStacked;
     // 64 columns of out and M leave room for a second S: the next chunk's is
     // formed before P Y of this one
     constexpr bool kTwoS = DB == 64;
     constexpr uint32_t kTmemO = kTwoS ? 384 : 256, kTmemM = kTwoS ? 448 : 384;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t x_full[2], y_full[2], z_free[2], x_free[2], y_free[2];  // x_full: Z and X
-    __shared__ uint64_t s_ready, m_ready, a_done, p_done, o_ready, o_free, drain_bar;
+    __shared__ uint64_t s_ready, m_ready, a_done, p_done, o_ready, o_free, sum_ready, drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]:
@@ -323,6 +337,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         mbar_init(smem_u32(&o_ready), 1);
         mbar_init(smem_u32(&m_ready), 1);
         mbar_init(smem_u32(&o_free), kLaWorkers);
+        mbar_init(smem_u32(&sum_ready), kLaWorkers / 2);
         mbar_init(smem_u32(&drain_bar), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -347,6 +362,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // decayed x of chunk c; without S its place serves every second chunk, so
     // that x is made ready while the chunk before is multiplied
     auto x_at = [&](int c) { return STATE && (c & 1) ? kTmemP : kTmemX; };
+    auto x_smem = [&](int c) { return base + Sh::oX + (STATE && (c & 1) ? Sh::kX : 0); };
     auto p_at = [&](int c) { return kTwoS && (c & 1) ? kTmemP2 : kTmemP; };
     auto chunk_at = [&](int c) { return P.reverse ? n_chunks - 1 - c : c; };
     auto rows_of = [&](int k) { return min(kC, n_tok - k * kC); };
@@ -357,7 +373,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     if (warp < kLaWorkers) {
         const int w4 = warp & 3, g4 = warp >> 2;
         const int row = w4 * 32 + lane, col0 = g4 * kN;
-        const bool fed = DA == 128 || w4 * 32 < DA;  // columns of X feed this lane quarter of the decayed x and of M
+        const bool fed = DA == 128 || kStacked || w4 * 32 < DA;  // columns of X feed this lane quarter of the decayed x and of M
         [[maybe_unused]] float top = 0.f;
         bool ok = true;
         if (!fed) {
@@ -459,7 +475,31 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             // (with two places for S it was formed long ago, of the loaded X)
             ok = !STATE && kTwoS ? waits(s_ready, c, kErrEpilogue) : waits(x_full[c & 1], c >> 1, kErrEpilogue);
             if (!ok) break;
-            if (fed) {
+            if constexpr (kStacked) {
+                if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
+                // 8 columns of a token at a time, in the tile's own places
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int e = threadIdx.x + i * kLaWorkers * 32, j = e >> 3;
+                    const uint32_t at = (uint32_t)j * 128u + (uint32_t)((e ^ j) & 7) * 16u;
+                    uint32_t x[4], hi[4], lo[4];
+                    lds128(base + Sh::x(c) + at, x);
+                    // the factor of the last row forward in time (0 for tokens
+                    // after it), of the first one backward
+                    const float f = tab[0][(P.reverse ? kC - 1 : kC - n) + j] * (kUpX / kUp);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float2 v = __fmul2_rn(unpack2<T>(x[k]), make_float2(f, f));
+                        if (n < kC && j >= n) v = make_float2(0.f, 0.f);  // what lies after the end may be NaN
+                        split2<T>(v, hi[k], lo[k]);
+                        if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                    sts128(x_smem(c) + at, hi[0], hi[1], hi[2], hi[3]);
+                    sts128(x_smem(c) + 16384u + at, lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_async_smem();
+                if (!STATE) tmem_st_wait();
+            } else if (fed) {
                 // the factors of the last row forward in time (0 for tokens
                 // after it), of the first one backward
                 const int at = (P.reverse ? kC - 1 : kC - n) + j0;
@@ -522,7 +562,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             if constexpr (!STATE) {
                 // ------------------------------------------- A: M's parts
                 if (fed) {
-                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)row * 128u;
+                    const uint32_t at = base + Sh::oM + (uint32_t)(col0 >> 6) * (DA * 128u) + (uint32_t)(row & (DA - 1)) * 128u;
 #pragma unroll
                     for (int k = 0; k < kN / 8; ++k) {
                         uint32_t hi[4], lo[4];
@@ -533,6 +573,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                             if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(m.x), fabsf(m.y)));
                         }
                         const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(row & 7)) * 16u;
+                        if (kStacked && w4 >= 2) {  // the sum of lo products: 2^-9 of M, its hi part is enough
+                            sts128(at + 2 * Sh::kM + o, hi[0], hi[1], hi[2], hi[3]);
+                            continue;
+                        }
                         sts128(at + o, hi[0], hi[1], hi[2], hi[3]);
                         sts128(at + Sh::kM + o, lo[0], lo[1], lo[2], lo[3]);
                     }
@@ -594,6 +638,27 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
                 tmem_ld_wait();
                 rescale();
+            }
+        }
+        if constexpr (kStacked) {
+            if (ok && m_out) {  // the two sums joined; M's parts are not read any more
+                const uint32_t at = base + Sh::oM + (uint32_t)((row & 63) * 64 + col0) * 4u;
+                if (w4 >= 2) {
+#pragma unroll
+                    for (int i = 0; i < kN; i += 4)
+                        sts128(at + i * 4, __float_as_uint(mv[i]), __float_as_uint(mv[i + 1]), __float_as_uint(mv[i + 2]),
+                               __float_as_uint(mv[i + 3]));
+                    warp_arrive(sum_ready, lane);
+                } else {
+                    ok = waits(sum_ready, 0, kErrEpilogue);
+#pragma unroll
+                    for (int i = 0; i < kN; i += 4) {
+                        uint32_t u[4];
+                        lds128(at + i * 4, u);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mv[i + k] += __uint_as_float(u[k]);
+                    }
+                }
             }
         }
         if (ok && m_out && row < P.Da) {
@@ -683,7 +748,13 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             if (!STATE && !kTwoS && c > 0 && !form_s(c)) break;
             if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
             tc_fence_after();
-            by_y(tmem + kTmemM, tmem + x_at(c), c);
+            if constexpr (kStacked) {
+                const uint64_t xd = desc_mn(x_smem(c), 16384), yd = desc_mn(base + Sh::y(c), 16384);
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k) mma_ss_one(tmem + kTmemM, xd + 128 * k, yd + 128 * k, P.idesc_n | (1u << 15), 1);
+            } else {
+                by_y(tmem + kTmemM, tmem + x_at(c), c);
+            }
             if constexpr (!STATE) {
                 if (!wait1(o_free, c)) break;
                 tc_fence_after();
@@ -694,6 +765,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     const uint32_t o = (k / 4) * 1024 + (k & 3) * 2;
                     mma_ss_one(tmem + kTmemO, zd + o, mh + 128 * k, P.idesc_n, k > 0);
                     mma_ss_one(tmem + kTmemO, zd + o, ml + 128 * k, P.idesc_n, 1);
+                    if constexpr (kStacked) mma_ss_one(tmem + kTmemO, zd + o, ml + (Sh::kM >> 4) + 128 * k, P.idesc_n, 1);
                 }
                 commit_one(z_free[s]);
                 commit_one(m_ready);  // the new M and Z M
