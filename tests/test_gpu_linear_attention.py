@@ -222,3 +222,38 @@ def test_a_wait_that_gives_up_is_reported(dtype):
     again = ct.linear_attention(q, k, v, ld, s)
     assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
     assert ct.ct_device_status(clear=True) == (ct.CT_OK, 0)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [64, 128, 48])
+def test_unequal_lengths_in_segments(dtype, D):
+    """Few heads, so that sequences are cut into segments, some of them behind a sequence's end."""
+    run_all(D, 3, 1700, 1, D, D, dtype, lengths=[0, 700, 1700])
+    run_all(D + 1, 2, 1100, 1, D, D, dtype, lengths=[1024, 1], states=False)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("T", [1, 90, 1500])
+def test_first_gradient_over_the_last(dtype, T):
+    """dstate_in written over dstate_out, and a workspace of the call's own, through the C entry point."""
+    B, H, D = 2, 1, 64
+    q, k, v, do, ld, s, ds = inputs(T, B, T, H, D, D, dtype)
+    want = ct.linear_attention_backward(q, k, v, ld, do, s, ds)
+    st = ct.block._I64x3(T * H * D, H * D, D)
+    over, out = ds.clone(), [torch.empty_like(q) for _ in range(3)]
+    rc = ct.lib().ct_linear_attention_backward(
+        q.data_ptr(), st, k.data_ptr(), st, v.data_ptr(), st, do.data_ptr(), st, ld.data_ptr(), s.data_ptr(), over.data_ptr(), None,
+        out[0].data_ptr(), st, out[1].data_ptr(), st, out[2].data_ptr(), st, over.data_ptr(), None, 0, B, T, H, D, D, D ** -0.5,
+        ct.dtype_code(q.dtype), torch.cuda.current_stream().cuda_stream)
+    assert rc == ct.CT_OK
+    n = None
+    check_attention_back(dtype, q, k, v, ld, do, s, ds, n, D ** -0.5, *out, over)
+    for a, b in zip(want[:3], out):
+        assert a.shape == b.shape
+    # a workspace that is too small is refused
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    if T == 1500:
+        rc = ct.lib().ct_linear_attention_forward(
+            q.data_ptr(), st, k.data_ptr(), st, v.data_ptr(), st, out[0].data_ptr(), st, ld.data_ptr(), None, None, None, ws.data_ptr(),
+            256, B, T, H, D, D, 1.0, ct.dtype_code(q.dtype), torch.cuda.current_stream().cuda_stream)
+        assert rc == ct.ct.CT_ERR_WORKSPACE

@@ -216,12 +216,17 @@ cudaError_t launch(const ScanArgs& S, int segs, cudaStream_t s) {
     }
 }
 
-// Segments of the scan and the tokens of one: enough to bring about four
-// blocks to an SM, of at least 64 tokens (a segment's first pass costs about
-// 2/3 of its second, so fewer tokens than that gain nothing).
+// Segments of the scan and the tokens of one.  A segment is walked twice, and
+// the matrices between cost as much again where they are many (64 heads of
+// 128 x 128, 128 tokens: 127 us in several, 39 in one), so sequences are cut
+// only where two blocks to an SM leave room for four segments of at least 64
+// tokens (f32, heads of 64: 38 heads of 512 tokens in four 61 us, 39 in one 78;
+// of 256 tokens 40 and 41; 15 heads of 40 x 72, 333 tokens in five 41, in one
+// 78).
 void scan_split(int64_t BH, int64_t T, int64_t Db, int* segs, int* tokens) {
     const int64_t blocks = std::max<int64_t>(1, BH * ((Db + kCols - 1) / kCols));
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(608 / blocks, T / 64), 4096));
+    int64_t want = std::min<int64_t>(std::min<int64_t>(304 / blocks, T / 64), 4096);
+    if (want < 4) want = 1;
     *tokens = (int)std::max<int64_t>(1, (T + want - 1) / want);
     *segs = (int)std::max<int64_t>(1, (T + *tokens - 1) / *tokens);
 }

@@ -16,7 +16,9 @@
 // operands.  S is exact in its operands.  P, M and the decayed x are fp32
 // values, and each enters as hi + lo, two 16-bit numbers, in two MMAs: with
 // one rounding each, out's error would be 1.4 to 1.7 times that of rounding
-// out itself, and the fp32 state's 2^-9.  P and x enter from TMEM (P over S,
+// out itself, and the fp32 state's 2^-9; with two, both to nearest, a bf16
+// value keeps about 17 bits (an f16 one 22) and the state comes to about 3e-6
+// of its norm.  P and x enter from TMEM (P over S,
 // in place), M from shared memory.
 //
 // One CTA per sequence, head and segment walks its chunks in order.  Sixteen
@@ -29,13 +31,17 @@
 // under M's split, Z M under B.  Warps with a role each (P, x, M at the same
 // time) came first: their bodies evicted one another from the instruction
 // caches and a warp issued once in 13 cycles (8 x 2048 x 16 heads of 128:
-// 93 us).
+// 93 us; as it is, 69).
 // One more warp loads tiles by TMA into a ring of five that Z, X and Y take in
 // turn (X's place, once x is in TMEM, stages out for its TMA store), one issues
 // the MMAs.
-// Bound by memory at full occupancy: 4 x 128 x D x 2 bytes a chunk (5650
-// cycles of the SM's share of the copy rate at D = 128) against 3600 cycles of
-// MMAs.
+// What bounds it is the chain A, B, C of a chunk and the waits between its
+// steps, about 7000 cycles at D = 128 and 5200 at 64, one CTA to an SM; memory
+// would take 5650 (4 x 128 x D x 2 bytes at the SM's share of the copy rate)
+// and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
+// with first and last state 69 us (60% of the copy rate), 32768 tokens of 8
+// heads of 64 in 19 segments 91 us, the three gradients of 8 x 2048 x 8 heads
+// of 64 in one launch 96 us.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first
 // launch forms each segment's own sum (the last line above from M = 0), a
@@ -220,6 +226,17 @@ __device__ __forceinline__ void tmem_st_scaled(uint32_t taddr, const float* v, f
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Eight consecutive floats (32 bytes, aligned to that) as one access.
+__device__ __forceinline__ void load8(const float* p, float* v) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -454,13 +471,24 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             tmem_st32(lane_base + p_at(c) + p0, u);
         };
 
-        // this warp's part of M before the chunk at hand
+        // this warp's part of M before the chunk at hand: a thread has kN
+        // columns of a row, eight to an access where rows lie on 32 bytes
+        // (single ones touch a sector each: the segments' matrices of 128 x 128
+        // then cost more than their chunks)
         float mv[kN];
+        const bool wide = P.Db % 8 == 0 && ((uintptr_t)m_in | (uintptr_t)m_out) % 32 == 0;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int col = col0 + i;
-            mv[i] = 0.f;
-            if (m_in && row < P.Da && col < P.Db) mv[i] = m_in[P.m_in_t ? (int64_t)col * P.Da + row : (int64_t)row * P.Db + col];
+        for (int i = 0; i < kN; ++i) mv[i] = 0.f;
+        if (m_in && row < P.Da) {
+            if (wide && !P.m_in_t) {
+#pragma unroll
+                for (int i = 0; i < kN; i += 8)
+                    if (col0 + i < P.Db) load8(m_in + (int64_t)row * P.Db + col0 + i, mv + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    if (col0 + i < P.Db) mv[i] = m_in[P.m_in_t ? (int64_t)(col0 + i) * P.Da + row : (int64_t)row * P.Db + col0 + i];
+            }
         }
         auto rescale = [&] {  // what TMEM holds to M
             if constexpr (kHalf)
@@ -478,7 +506,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             if constexpr (kStacked) {
                 if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
                 // 8 columns of a token at a time, in the tile's own places
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     const int e = threadIdx.x + i * kLaWorkers * 32, j = e >> 3;
                     const uint32_t at = (uint32_t)j * 128u + (uint32_t)((e ^ j) & 7) * 16u;
@@ -664,8 +692,17 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         if (ok && m_out && row < P.Da) {
             const float last = P.reverse && P.final ? pw[1] : 1.f;
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-                if (col0 + i < P.Db) m_out[(int64_t)row * P.Db + col0 + i] = mv[i] * last;
+            for (int i = 0; i < kN; ++i) mv[i] *= last;
+            float* to = m_out + (int64_t)row * P.Db + col0;
+            if (wide) {
+#pragma unroll
+                for (int i = 0; i < kN; i += 8)
+                    if (col0 + i < P.Db) store8(to + i, mv + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    if (col0 + i < P.Db) to[i] = mv[i];
+            }
         }
         if constexpr (!STATE)
             if (ok && waits(o_ready, n_chunks - 1, kErrEpilogue)) {
@@ -869,11 +906,15 @@ cudaError_t launch_t(const LaTcBatch& Q, int cores, int dtype, cudaStream_t s) {
 }
 
 // Segments of a sequence, and the tokens of one: as many as fill the GPU once
-// with one CTA each, of at least four chunks (a segment costs a second read of
-// X and Y and a chain step).
+// with one CTA each, of at least four chunks.  A segment's X and Y are read
+// twice and its matrices pass through memory, so two segments do not pay
+// (2048 tokens, 76 heads of 128 in two: 90 us; 77 in one: 66; of 64: 55 and
+// 49), three do (39 heads of 128: 64 us, of 64: 42; four, 38 heads: 54 and 37;
+// 8192 tokens, 50 heads of 128 in three: 161 us; 77 in one: 235).
 void split(int64_t heads, int64_t T, int sm_count, int* segs, int* tokens) {
     const int64_t chunks = (T + kC - 1) / kC;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(sm_count / std::max<int64_t>(1, heads), chunks / 4));
+    int64_t want = std::min<int64_t>(sm_count / std::max<int64_t>(1, heads), chunks / 4);
+    if (want < 3) want = 1;
     const int64_t per = (chunks + want - 1) / want;
     *tokens = (int)(per * kC);
     *segs = (int)((chunks + per - 1) / per);
