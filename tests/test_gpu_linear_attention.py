@@ -257,3 +257,12 @@ def test_first_gradient_over_the_last(dtype, T):
             q.data_ptr(), st, k.data_ptr(), st, v.data_ptr(), st, out[0].data_ptr(), st, ld.data_ptr(), None, None, None, ws.data_ptr(),
             256, B, T, H, D, D, 1.0, ct.dtype_code(q.dtype), torch.cuda.current_stream().cuda_stream)
         assert rc == ct.ct.CT_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,T,H,Dk,Dv", [(7, 500, 23, 24, 40), (1, 1100, 155, 64, 64), (2, 300, 111, 72, 128), (19, 400, 9, 128, 33)])
+def test_more_walks_than_processors(dtype, B, T, H, Dk, Dv):
+    """Walks shared between processors: one begins a walk, the next ends it."""
+    run_all(B * T, B, T, H, Dk, Dv, dtype, states=T != 300)
+    lengths = [(97 * i) % (T + 1) for i in range(B)]
+    run_all(B * T + 1, B, T, H, Dk, Dv, dtype, lengths=lengths)

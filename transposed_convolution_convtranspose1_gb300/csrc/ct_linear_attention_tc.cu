@@ -39,14 +39,20 @@
 // steps, about 7000 cycles at D = 128 and 5200 at 64, one CTA to an SM; memory
 // would take 5650 (4 x 128 x D x 2 bytes at the SM's share of the copy rate)
 // and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
-// with first and last state 69 us (60% of the copy rate), 32768 tokens of 8
+// with the last state 69 us (60% of the copy rate), 32768 tokens of 8
 // heads of 64 in 19 segments 91 us, the three gradients of 8 x 2048 x 8 heads
-// of 64 in one launch 96 us.
+// of 64 in one launch 79 us.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first
 // launch forms each segment's own sum (the last line above from M = 0), a
 // small kernel chains them into the matrix before each segment, and the main
 // launch runs all segments at once.
+//
+// More walks than SMs: the chunks of all walks, one after another, are cut into
+// equal runs, one for each SM.  A walk cut by a run's end is begun by the one
+// CTA as its first piece and ended by the next CTA as its last, which takes the
+// matrix from memory; nothing is read twice (the gradients above: 192 walks of
+// 16 chunks, 21 chunks an SM instead of 32; 96 us in two turns).
 #include <algorithm>
 #include <cstring>
 
@@ -88,6 +94,11 @@ struct LaTcParams {
 struct LaTcBatch {
     LaTcParams core[3];
     int ctas;                    // of one core
+    // shared walks (quota > 0): the chunks of all walks in a row, cut into runs
+    // of `quota` chunks, one for each CTA of a cooperative launch
+    int quota, chunks, walks;    // chunks: of one walk; quota >= chunks
+    float* handed;               // [CTA][Da][Db]
+    unsigned* done;              // [CTA]: its first piece's matrix is there
 };
 
 // Tile n of the walk (Z, X, Y of chunk 0, Z, X, Y of chunk 1, ...) lies in
@@ -276,10 +287,26 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t sr
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Waits, for a limited time, until another CTA of the launch has set *done.
+__device__ __forceinline__ bool wait_done(const unsigned* done, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+        if (v) return true;
+        if (limit_ns == 0 || globaltimer_ns() - t0 > limit_ns) {
+            atomicOr(&g_device_error, kErrEpilogue);
+            return false;
+        }
+        __nanosleep(100);
+    }
+}
+
 template <typename T, int DA, int DB, bool STATE>
 __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcBatch Q) {
-    const LaTcParams& P = Q.core[blockIdx.x / (unsigned)Q.ctas];
-    const unsigned cta = blockIdx.x % (unsigned)Q.ctas;
     using Sh = LaShape<DA, DB>;
     constexpr bool kHalf = std::is_same<T, __half>::value;
     // f16 scores and decayed x are kept 16 and 64 times their size: the lo
@@ -303,10 +330,47 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     __shared__ float pw[kC + 2];    // decay^k
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the tiles' swizzle needs 1024-byte alignment, which the declaration asks
+    // for; there is no room to round up (227 KiB are used at 128 x 128)
+    const uint32_t base = smem_u32(smem_raw);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_device_error, kErrProducer);
+        return;
+    }
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (warp == kLaWorkers + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    // One piece, a whole walk or segment, without a quota.  With one, the run's
+    // pieces from its end to its start: the first may be a walk's beginning,
+    // handed to the next CTA, the last a walk's end, begun by the CTA before,
+    // which had it done before this one's other pieces: quota >= chunks.
+    const int run0 = (int)blockIdx.x * Q.quota;
+    int run = min(run0 + Q.quota, Q.walks * Q.chunks);
+    do {
+    unsigned cta = blockIdx.x;
+    int w0 = 0, w1 = 0;  // the piece's chunks of its walk
+    if (Q.quota) {
+        cta = (unsigned)(run - 1) / (unsigned)Q.chunks;
+        const int walk0 = (int)cta * Q.chunks, from = max(run0, walk0);
+        w0 = from - walk0;
+        w1 = run - walk0;
+        run = from;
+    }
+    const LaTcParams& P = Q.core[cta / (unsigned)Q.ctas];
+    cta %= (unsigned)Q.ctas;
     const int bh = (int)(cta % (unsigned)P.BH), seg = (int)(cta / (unsigned)P.BH);
     const int b = bh / P.H, h = bh % P.H;
     const int len = P.lengths ? max(0, min(P.T, P.lengths[b])) : P.T;
-    const int s0 = seg * P.seg_tokens, s1 = min(P.T, s0 + P.seg_tokens);
+    const int s0 = Q.quota ? (P.reverse ? Q.chunks - w1 : w0) * kC : seg * P.seg_tokens;
+    const int s1 = min(P.T, Q.quota ? s0 + (w1 - w0) * kC : s0 + P.seg_tokens);
     const int n_tok = max(0, min(len, s1) - s0);
     const int n_chunks = (n_tok + kC - 1) / kC;
     const int64_t msize = (int64_t)P.Da * P.Db;
@@ -322,25 +386,20 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         T* out = static_cast<T*>(P.out) + b * P.os[0] + h * P.os[2];
         for (int64_t i = threadIdx.x; i < rows * P.Db; i += kLaThreads) out[(from + i / P.Db) * P.os[1] + i % P.Db] = from_f32<T>(0.f);
     }
-    const float* m_in = P.m_in ? P.m_in + (P.m_in_seg ? ((int64_t)seg * P.BH + bh) * msize : bh * msize) : nullptr;
-    float* m_out = P.m_out ? P.m_out + ((int64_t)seg * P.BH + bh) * msize : nullptr;
-    if (n_chunks == 0) {  // the same for every thread
-        if (m_out)
-            for (int64_t i = threadIdx.x; i < msize; i += kLaThreads)
-                m_out[i] = m_in ? (P.m_in_t ? m_in[(i % P.Db) * P.Da + i / P.Db] : m_in[i]) : 0.f;
-        return;
-    }
+    const bool begun = w0 > 0, handed = w1 < Q.chunks;  // the CTA before, the next one has the rest
+    bool late = false;
+    if (begun && threadIdx.x == 0) late = !wait_done(Q.done + blockIdx.x - 1, P.wait_ns);
+    if (__syncthreads_or(late)) break;
+    const float* m_in = begun ? Q.handed + (blockIdx.x - 1) * msize : P.m_in ? P.m_in + (P.m_in_seg ? ((int64_t)seg * P.BH + bh) * msize : bh * msize) : nullptr;
+    const bool m_in_t = P.m_in_t && !begun, last_piece = P.final && !handed;
+    float* m_out = handed ? Q.handed + blockIdx.x * msize : P.m_out ? P.m_out + ((int64_t)seg * P.BH + bh) * msize : nullptr;
+    if (n_chunks == 0 && m_out)  // (the same for every thread)
+        for (int64_t i = threadIdx.x; i < msize; i += kLaThreads)
+            m_out[i] = m_in ? (m_in_t ? m_in[(i % P.Db) * P.Da + i / P.Db] : m_in[i]) : 0.f;
+    if (n_chunks > 0) {
 
     const float g = fmaxf(P.log_decay[h], -1e30f);
-    // the tiles' swizzle needs 1024-byte alignment, which the declaration asks
-    // for; there is no room to round up (227 KiB are used at 128 x 128)
-    const uint32_t base = smem_u32(smem_raw);
-    if (base & 1023u) {
-        if (threadIdx.x == 0) atomicOr(&g_device_error, kErrProducer);
-        return;
-    }
     if (threadIdx.x == 0) {
-        abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&y_full[i]), 1);
             mbar_init(smem_u32(&y_free[i]), 1);
@@ -366,15 +425,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         tab[0][i] = f;
         if (i > 0) tab[1][i - 1] = f;
     }
-    if (warp == kLaWorkers + 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     // decayed x of chunk c; without S its place serves every second chunk, so
     // that x is made ready while the chunk before is multiplied
@@ -480,14 +533,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
 #pragma unroll
         for (int i = 0; i < kN; ++i) mv[i] = 0.f;
         if (m_in && row < P.Da) {
-            if (wide && !P.m_in_t) {
+            if (wide && !m_in_t) {
 #pragma unroll
                 for (int i = 0; i < kN; i += 8)
                     if (col0 + i < P.Db) load8(m_in + (int64_t)row * P.Db + col0 + i, mv + i);
             } else {
 #pragma unroll
                 for (int i = 0; i < kN; ++i)
-                    if (col0 + i < P.Db) mv[i] = m_in[P.m_in_t ? (int64_t)(col0 + i) * P.Da + row : (int64_t)row * P.Db + col0 + i];
+                    if (col0 + i < P.Db) mv[i] = m_in[m_in_t ? (int64_t)(col0 + i) * P.Da + row : (int64_t)row * P.Db + col0 + i];
             }
         }
         auto rescale = [&] {  // what TMEM holds to M
@@ -690,7 +743,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             }
         }
         if (ok && m_out && row < P.Da) {
-            const float last = P.reverse && P.final ? pw[1] : 1.f;
+            const float last = P.reverse && last_piece ? pw[1] : 1.f;
 #pragma unroll
             for (int i = 0; i < kN; ++i) mv[i] *= last;
             float* to = m_out + (int64_t)row * P.Db + col0;
@@ -780,7 +833,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             return true;
         };
         bool ok = STATE || form_s(0);
-        for (int c = 0; c < n_chunks && ok; ++c) {
+        int c = 0;
+        for (; c < n_chunks && ok; ++c) {
             const int s = c & 1;
             if (!STATE && !kTwoS && c > 0 && !form_s(c)) break;
             if (!wait1(y_full[s], c >> 1) || !wait1(a_done, c)) break;
@@ -820,8 +874,44 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         // no MMA may be in flight when TMEM is released
         commit_one(drain_bar);
         mbar_drain(smem_u32(&drain_bar), 0);
+        // nor any arrival, before the barriers are made anew
+        if (c == n_chunks)
+            for (int i = max(0, c - 2); i < c; ++i) {
+                mbar_drain(smem_u32(&y_free[i & 1]), (i >> 1) & 1);
+                mbar_drain(smem_u32(&x_free[i & 1]), (i >> 1) & 1);
+                if (!STATE) mbar_drain(smem_u32(&z_free[i & 1]), (i >> 1) & 1);
+            }
         __syncwarp();
     }
+    }
+    // nothing of the piece is in flight any more
+    tc_fence_before();
+    if (__syncthreads_or(abort_flag)) break;
+    tc_fence_after();
+    if (threadIdx.x == 0) {
+        if (n_chunks > 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_inval(smem_u32(&y_full[i]));
+                mbar_inval(smem_u32(&y_free[i]));
+                mbar_inval(smem_u32(&z_free[i]));
+                mbar_inval(smem_u32(&x_full[i]));
+                mbar_inval(smem_u32(&x_free[i]));
+            }
+            mbar_inval(smem_u32(&s_ready));
+            mbar_inval(smem_u32(&a_done));
+            mbar_inval(smem_u32(&p_done));
+            mbar_inval(smem_u32(&o_ready));
+            mbar_inval(smem_u32(&m_ready));
+            mbar_inval(smem_u32(&o_free));
+            mbar_inval(smem_u32(&sum_ready));
+            mbar_inval(smem_u32(&drain_bar));
+        }
+        if (handed) {  // every thread's part was stored before the barrier above
+            __threadfence();
+            asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(Q.done + blockIdx.x), "r"(1u) : "memory");
+        }
+    }
+    } while (run > run0);
 
     tc_fence_before();
     __syncthreads();
@@ -889,6 +979,12 @@ cudaError_t launch_k(const LaTcBatch& Q, int cores, cudaStream_t s) {
     constexpr int bytes = (int)LaShape<DA, DB>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
+    if (Q.quota) {  // CTAs that wait for others: all of them on the GPU at once
+        const unsigned grid = (unsigned)(((int64_t)Q.walks * Q.chunks + Q.quota - 1) / Q.quota);
+        LaTcBatch copy = Q;
+        void* args[] = {&copy};
+        return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(k), dim3(grid), dim3(kLaThreads), args, bytes, s);
+    }
     k<<<(unsigned)(Q.ctas * cores), kLaThreads, bytes, s>>>(Q);
     return cudaGetLastError();
 }
@@ -920,6 +1016,24 @@ void split(int64_t heads, int64_t T, int sm_count, int* segs, int* tokens) {
     *segs = (int)((chunks + per - 1) / per);
 }
 
+// More walks than SMs: the chunks a CTA gets where walks are shared, 0 where
+// each has its own CTA and the last turn leaves SMs empty.  A further piece
+// costs a CTA 5 to 8 us (tables, first loads, the matrix through memory), so
+// the chunks saved have to be two and a sixth of the quota.  bf16, 2048
+// tokens, us shared / two turns: 160 heads of 128 86 / 138, 228 125 / 138, 256
+// (27 chunks of 32) 146 / 138; 192 heads of 64 80 / 101, 256 100 / 101; 300
+// tokens, 192 heads of 128 38 / 43.
+int share(int64_t walks, int64_t T, int sm_count) {
+    const int64_t chunks = (T + kC - 1) / kC;
+    if (walks <= sm_count || walks * chunks >= (1ll << 30)) return 0;
+    const int64_t quota = (walks * chunks + sm_count - 1) / sm_count, turns = (walks + sm_count - 1) / sm_count;
+    return turns * chunks - quota >= 2 + quota / 6 ? (int)quota : 0;
+}
+
+size_t shared_bytes(int64_t msize, int sm_count) {
+    return round256((size_t)sm_count * msize * sizeof(float)) + round256((size_t)sm_count * sizeof(unsigned));
+}
+
 size_t core_bytes(int64_t BH, int64_t msize, int segs, int dtype) {
     const size_t m = (size_t)BH * msize * sizeof(float);
     return (segs > 1 ? round256(m * segs) : 0) + (dtype == CT_F16 ? round256(m) + round256((size_t)BH * sizeof(int)) : 0);
@@ -948,7 +1062,8 @@ size_t la_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_
     for (int cores = 1; cores <= (backward ? 3 : 1); ++cores) {
         int segs;
         split(B * H * cores, T, sm, &segs, &tokens);
-        most = std::max(most, cores * core_bytes(B * H, Dk * Dv, segs, dtype));
+        const size_t extra = share(B * H * cores, T, sm) ? shared_bytes(Dk * Dv, sm) : 0;
+        most = std::max(most, cores * core_bytes(B * H, Dk * Dv, segs, dtype) + extra);
     }
     return most;
 }
@@ -1032,6 +1147,15 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
             P.m_out = C.core[i].m_out;
             P.final = 1;
         }
+    }
+    Q.quota = share(BH * n, one.T, d.sm_count);
+    if (Q.quota) {
+        Q.chunks = (int)((one.T + kC - 1) / kC);
+        Q.walks = (int)(BH * n);
+        Q.handed = reinterpret_cast<float*>(ws);
+        Q.done = reinterpret_cast<unsigned*>(ws + round256((size_t)d.sm_count * msize * sizeof(float)));
+        e = cudaMemsetAsync(Q.done, 0, (size_t)d.sm_count * sizeof(unsigned), s);
+        if (e != cudaSuccess) return e;
     }
     if (segs > 1) {
         e = launch_t<true>(Q, n, one.dtype, s);
