@@ -8,6 +8,7 @@ libct.so on the current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -353,14 +354,19 @@ def _heads(t: Optional[torch.Tensor], shape, dtype):
     """(pointer, strides of batch, token and head) of a [B, T, H, D] tensor."""
     if t is None:
         return None, None
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise CtError(CT_ERR_SHAPE, f"expected shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise CtError(CT_ERR_DTYPE, f"expected {dtype}, got {t.dtype}")
-    st = t.stride()
-    if st[3] != 1 and shape[3] > 1:
+    b, s, h, d = t.stride()
+    if d != 1 and shape[3] > 1:
         raise ValueError("the last axis must be dense")
-    return t.data_ptr(), _I64x3(st[0], st[1], st[2])
+    return t.data_ptr(), _strides(b, s, h)
+
+
+@functools.lru_cache(maxsize=256)
+def _strides(b: int, t: int, h: int):
+    return _I64x3(b, t, h)
 
 
 def _attention_problem(q, v, log_decay, lengths, *states):
@@ -378,10 +384,12 @@ def _attention_problem(q, v, log_decay, lengths, *states):
     return B, T, H, Dk, Dv
 
 
-def _attention_workspace(B, T, H, Dk, Dv, code, backward, dev):
+@functools.lru_cache(maxsize=256)
+def _attention_workspace_bytes(B, T, H, Dk, Dv, code, backward, index):
     n = ctypes.c_size_t(0)
-    _check(lib().ct_linear_attention_workspace_bytes(B, T, H, Dk, Dv, code, backward, ctypes.byref(n)))
-    return (torch.empty((n.value,), dtype=torch.uint8, device=dev) if n.value else None), n.value
+    with torch.cuda.device(index):
+        _check(lib().ct_linear_attention_workspace_bytes(B, T, H, Dk, Dv, code, backward, ctypes.byref(n)))
+    return n.value
 
 
 def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -403,14 +411,14 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     pk, sk = _heads(k, (B, T, H, Dk), dt)
     pv, sv = _heads(v, (B, T, H, Dv), dt)
     index = _index_of(q, k, v, log_decay, state, lengths, state_out)
-    dev = q.device
-    o = torch.empty((B, T, H, Dv), dtype=dt, device=dev)
+    o = _like(v)
     if state_out is None and "state" in need:
-        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+        state_out = _like(state) if state is not None else torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
     code = dtype_code(dt)
-    ws, nws = _attention_workspace(B, T, H, Dk, Dv, code, 0, dev)
-    _call(lib().ct_linear_attention_forward, index, stream, pq, sq, pk, sk, pv, sv, _dense(o),
-          _I64x3(T * H * Dv, H * Dv, Dv), _dense(log_decay), _dense(state), _dense(state_out), _dense(lengths),
+    nws = _attention_workspace_bytes(B, T, H, Dk, Dv, code, 0, index)
+    ws = torch.empty((nws,), dtype=torch.uint8, device=q.device) if nws else None
+    _call(lib().ct_linear_attention_forward, index, stream, pq, sq, pk, sk, pv, sv, o.data_ptr(),
+          _strides(T * H * Dv, H * Dv, Dv), _dense(log_decay), _dense(state), _dense(state_out), _dense(lengths),
           _dense(ws), nws, B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
     return o, state_out
 
@@ -436,9 +444,10 @@ def linear_attention_backward(q, k, v, log_decay, do, state=None, dstate=None, l
     dfirst = None
     if "dstate" in need and state is not None:
         dfirst = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-    sqk, svv = _I64x3(T * H * Dk, H * Dk, Dk), _I64x3(T * H * Dv, H * Dv, Dv)
+    sqk, svv = _strides(T * H * Dk, H * Dk, Dk), _strides(T * H * Dv, H * Dv, Dv)
     code = dtype_code(dt)
-    ws, nws = _attention_workspace(B, T, H, Dk, Dv, code, 1, dev)
+    nws = _attention_workspace_bytes(B, T, H, Dk, Dv, code, 1, index)
+    ws = torch.empty((nws,), dtype=torch.uint8, device=dev) if nws else None
     _call(lib().ct_linear_attention_backward, index, stream, pq, sq, pk, sk, pv, sv, po, so, _dense(log_decay),
           _dense(state), _dense(dstate), _dense(lengths), _dense(dq), sqk, _dense(dk), sqk, _dense(dv), svv,
           _dense(dfirst), _dense(ws), nws, B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
