@@ -205,3 +205,12 @@ def test_forward_of_many_rows(cols, dtype):
                                       torch.cuda.current_stream().cuda_stream)
     assert rc == ct.CT_OK and torch.equal(stream, h) and torch.equal(y2, y)
     assert torch.equal(ct.rms_norm(x, None, None)[0], ct.rms_norm(x, None, None)[0])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [257, 300, 511, 513, 1025, 1500, 2047, 2049, 4097, 8191, 8193, 16385])
+def test_odd_widths(cols, dtype):
+    """Rows off 16-byte boundaries on both sides of every width at which another kernel takes over."""
+    test_forward(37, cols, dtype)
+    test_backward(37, cols, dtype)
+    test_8_bit_output(9, cols, 128, "int8", dtype)

@@ -28,8 +28,9 @@ struct ScanArgs {
 // the columns a lane still carries) and, across the four warps, through shared
 // memory once per TB tokens; the next TB tokens' values are on their way in
 // registers meanwhile.  A streaming step (one token) is bound by memory, the
-// state read and written: 64 x 8 heads of 128 x 128, 20 us (134 MB).  Longer
-// sequences are bound by each token's chain of sums.
+// state read and written: 64 x 8 heads of 128 x 128, 67 MB, 15 us, 66% of the
+// copy rate (256 x 8 heads 52 us, 77%).  Longer sequences are bound by each
+// token's chain of sums.
 template <typename T, int RX, int TB>
 __global__ void __launch_bounds__(kWarps * 32) la_scan(const __grid_constant__ ScanArgs S) {
     const LaCore& A = S.c;
@@ -201,7 +202,7 @@ cudaError_t launch_tb(const ScanArgs& S, int segs, cudaStream_t s) {
 }
 
 // Streaming steps stage four tokens: fewer registers, so more of the state in
-// flight (64 x 8 heads of 128 x 128: 26 us with sixteen).
+// flight (64 x 8 heads of 128 x 128, with the call: 21 us; 26 with sixteen).
 template <typename T>
 cudaError_t launch_t(const ScanArgs& S, int segs, cudaStream_t s) {
     return S.c.T <= 4 ? launch_tb<T, 4>(S, segs, s) : launch_tb<T, 16>(S, segs, s);
