@@ -608,7 +608,9 @@ int ct_conv_transpose_nd_noalloc(const void* x, const void* w, const void* bias,
 /*
  * Device-side error word written by bounded waits in the kernels that wait on
  * asynchronous copies or MMAs (0 = none; otherwise the bits say which wait
- * gave up: 1 TMA producer, 2 MMA issuer, 4 epilogue (tensor-core routes),
+ * gave up: 1 TMA producer, 2 MMA issuer, 4 epilogue (tensor-core routes, the
+ * worker warps of linear attention in chunks and their wait for another
+ * block's matrix),
  * 8 a drain after a give-up that itself ran out, 16 the grouped TMA kernel's
  * copy, 32 a grouped warp pair's input copy, 64 a grouped warp pair's results,
  * 128 a staged copy of the backward pass's small-group weight-gradient

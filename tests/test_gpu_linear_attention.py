@@ -266,3 +266,27 @@ def test_more_walks_than_processors(dtype, B, T, H, Dk, Dv):
     run_all(B * T, B, T, H, Dk, Dv, dtype, states=T != 300)
     lengths = [(97 * i) % (T + 1) for i in range(B)]
     run_all(B * T + 1, B, T, H, Dk, Dv, dtype, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_shared_walks_in_a_graph(dtype):
+    """The launch whose blocks wait for one another, captured and replayed on other values."""
+    B, T, H, D = 4, 700, 60, 64
+    q, k, v, do, ld, s, ds = inputs(5, B, T, H, D, D, dtype)
+    held = [t.clone() for t in (q, k, v, do)]
+    ct.linear_attention_backward(*held[:3], ld, held[3], s, ds)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, last = ct.linear_attention(*held[:3], ld, s)
+        got = ct.linear_attention_backward(*held[:3], ld, held[3], s, ds)
+    for seed in (6, 7):
+        new = inputs(seed, B, T, H, D, D, dtype)
+        for h, n in zip(held, new):
+            h.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        eo, elast = ct.linear_attention(*new[:3], ld, s)
+        eager = ct.linear_attention_backward(*new[:3], ld, new[3], s, ds)
+        for a, b in zip((o, last, *got), (eo, elast, *eager)):
+            assert torch.equal(a, b)

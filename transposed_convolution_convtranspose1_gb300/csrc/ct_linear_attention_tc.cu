@@ -31,7 +31,7 @@
 // under M's split, Z M under B.  Warps with a role each (P, x, M at the same
 // time) came first: their bodies evicted one another from the instruction
 // caches and a warp issued once in 13 cycles (8 x 2048 x 16 heads of 128:
-// 93 us; as it is, 69).
+// 93 us; as it is, 67).
 // One more warp loads tiles by TMA into a ring of five that Z, X and Y take in
 // turn (X's place, once x is in TMEM, stages out for its TMA store), one issues
 // the MMAs.
@@ -39,8 +39,8 @@
 // steps, about 7000 cycles at D = 128 and 5200 at 64, one CTA to an SM; memory
 // would take 5650 (4 x 128 x D x 2 bytes at the SM's share of the copy rate)
 // and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
-// with the last state 69 us (60% of the copy rate), 32768 tokens of 8
-// heads of 64 in 19 segments 91 us, the three gradients of 8 x 2048 x 8 heads
+// with the last state 67 us (61% of the copy rate), 32768 tokens of 8
+// heads of 64 in 19 segments 94 us, the three gradients of 8 x 2048 x 8 heads
 // of 64 in one launch 79 us.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first
