@@ -40,7 +40,7 @@
 // would take 5650 (4 x 128 x D x 2 bytes at the SM's share of the copy rate)
 // and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
 // with the last state 67 us (61% of the copy rate), 32768 tokens of 8
-// heads of 64 in 19 segments 94 us, the three gradients of 8 x 2048 x 8 heads
+// heads of 64 in 19 segments 90 us, the three gradients of 8 x 2048 x 8 heads
 // of 64 in one launch 79 us.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first
@@ -251,6 +251,11 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
 }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ float2 lds64(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -502,9 +507,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             } else {
                 float v[32];
                 tmem_ld32(lane_base + p_at(c) + p0, v);
-                tmem_ld_wait();
+                // the factors are on their way while S is (the MMAs' own reads
+                // of shared memory make theirs slow)
                 const int at = (kC - 1) + p0 - row;
-                const float2* f = reinterpret_cast<const float2*>(tab[at & 1] + (at & ~1));
+                const uint32_t ft = smem_u32(tab[at & 1] + (at & ~1));
+                float2 f[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = lds64(ft + 8 * i);
+                tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 m = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f[i]);
@@ -558,19 +568,29 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             if (!ok) break;
             if constexpr (kStacked) {
                 if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
-                // 8 columns of a token at a time, in the tile's own places
-#pragma unroll 1
+                // 8 columns of a token at a time, in the tile's own places, the
+                // second ones loaded before the first are split
+                const int j0 = threadIdx.x >> 3;
+                const uint32_t at0 = (uint32_t)j0 * 128u + (uint32_t)((threadIdx.x ^ j0) & 7) * 16u;
+                // the factor of the last row forward in time (0 for tokens
+                // after it), of the first one backward
+                const float* ft = tab[0] + (P.reverse ? kC - 1 : kC - n) + j0;
+                uint32_t x[2][4];
+                float fx[2];
+#pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int e = threadIdx.x + i * kLaWorkers * 32, j = e >> 3;
-                    const uint32_t at = (uint32_t)j * 128u + (uint32_t)((e ^ j) & 7) * 16u;
-                    uint32_t x[4], hi[4], lo[4];
-                    lds128(base + Sh::x(c) + at, x);
-                    // the factor of the last row forward in time (0 for tokens
-                    // after it), of the first one backward
-                    const float f = tab[0][(P.reverse ? kC - 1 : kC - n) + j] * (kUpX / kUp);
+                    lds128(base + Sh::x(c) + at0 + i * 8192u, x[i]);
+                    fx[i] = ft[i * 64] * (kUpX / kUp);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = j0 + i * 64;
+                    const uint32_t at = at0 + i * 8192u;
+                    uint32_t hi[4], lo[4];
+                    const float f = fx[i];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float2 v = __fmul2_rn(unpack2<T>(x[k]), make_float2(f, f));
+                        float2 v = __fmul2_rn(unpack2<T>(x[i][k]), make_float2(f, f));
                         if (n < kC && j >= n) v = make_float2(0.f, 0.f);  // what lies after the end may be NaN
                         split2<T>(v, hi[k], lo[k]);
                         if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
