@@ -36,7 +36,7 @@
 // turn (X's place, once x is in TMEM, stages out for its TMA store), one issues
 // the MMAs.
 // What bounds it is the chain A, B, C of a chunk and the waits between its
-// steps, about 7000 cycles at D = 128 and 5200 at 64, one CTA to an SM; memory
+// steps, about 7000 cycles at D = 128 and 4700 at 64, one CTA to an SM; memory
 // would take 5650 (4 x 128 x D x 2 bytes at the SM's share of the copy rate)
 // and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
 // with the last state 67 us (61% of the copy rate), 32768 tokens of 8

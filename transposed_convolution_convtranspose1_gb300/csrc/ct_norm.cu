@@ -528,10 +528,11 @@ bool rows16(const void* p, int64_t stride, size_t eb, int64_t rows) {
 // hold it, so that blocks stay small and rows many.  Measured on 2^25 bf16
 // elements with residual, h and int8 codes (us, this / the next wider): 512
 // columns in one warp of two vectors a thread 49 / 62 in four; 2048 in 128
-// threads 48.  Rows off 16-byte boundaries go element by element (2048 columns
-// 122 us), and beyond 2048 columns through norm_fwd_rows, whose second pass
-// finds the row in L1: 2056 columns 107 us against 677 in registers, 4096 97
-// against 355, 8192 101 against 196.
+// threads 48.  Rows off 16-byte boundaries go element by element (1024 columns
+// 122 us; 512 in 64 threads 122, in 128 171), and beyond 1024 columns through
+// norm_fwd_rows, whose second pass finds the row in L1: 1032 columns 138 us
+// against 179 in registers, 2048 101 against 122, 4096 97 against 355, 8192 101
+// against 196.
 template <typename T>
 cudaError_t launch_fwd(const NormFwd& A, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
