@@ -41,7 +41,7 @@
 // and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
 // with the last state 67 us (61% of the copy rate), 32768 tokens of 8
 // heads of 64 in 19 segments 90 us, the three gradients of 8 x 2048 x 8 heads
-// of 64 in one launch 79 us.
+// of 64 in one launch 80 us.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first
 // launch forms each segment's own sum (the last line above from M = 0), a
