@@ -3,7 +3,9 @@ RMS norm, 8-bit activation checkpoints with the (gated) activation that uses
 them, and linear attention with a decay for each head (include/ct.h).
 
 Argument marshalling only, as in ct.py: every step of the computation runs in
-libct.so on the current stream of the tensors' device.
+libct.so on the current stream of the tensors' device.  A call given `stream`
+runs as if that were the current one, outputs included: as after any work on a
+side stream, the caller orders the streams around it.
 """
 from __future__ import annotations
 
@@ -52,12 +54,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _call(fn, index, stream, *args):
-    """fn(*args, stream) with the tensors' device current."""
-    if stream is None and _raw_stream is not None:
-        s = _raw_stream(index)
-    else:
-        s = _stream_handle(stream, torch.device("cuda", index))
+def _call(fn, index, *args):
+    """fn(*args, stream) on the current stream of the tensors' device, which is made current."""
+    s = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
     if index == (_get_device() if _get_device is not None else torch.cuda.current_device()):
         rc = fn(*args, s)
     else:
@@ -65,6 +64,20 @@ def _call(fn, index, stream, *args):
             rc = fn(*args, s)
     if rc:
         _check(rc)
+
+
+def _on(stream, first):
+    """`stream` (a torch stream or a raw handle) as the current one.  A call's
+    outputs and workspace come from the allocator's pool of the current stream
+    and are free for reuse in that stream's order: taken from another stream's
+    pool, a workspace would be handed out again while kernels still use it."""
+    index = _index_of(first)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream, None)
+        stream = torch.cuda.ExternalStream(handle, index) if handle else torch.cuda.default_stream(index)
+    if stream.device.index != index:
+        raise CtError(CT_ERR_PARAM, f"the stream is of {stream.device}, the tensors are on cuda:{index}")
+    return torch.cuda.stream(stream)
 
 
 def _rows(t: Optional[torch.Tensor], like: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None):
@@ -177,6 +190,9 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     in 8 bits where `quant` is "int8" or "e4m3".  y and rstd are None unless
     named in `need`.
     """
+    if stream is not None:
+        with _on(stream, x):
+            return rms_norm(x, weight, residual, eps, quant, group, need)
     q = _quant(quant)
     px, sx = _rows(x)
     pr, sr = _rows(residual, x, x.dtype)
@@ -187,7 +203,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     h = _like(x) if residual is not None else None
     rstd = torch.empty(rows if x.dim() == 2 else x.shape[:-1], dtype=torch.float32, device=x.device) if "rstd" in need else None
     kept = _new_checkpoint(x, q, group) if q != CT_Q_NONE else None
-    _call(lib().ct_rms_norm_forward, index, stream, px, sx, pr, sr, _dense(weight), y.data_ptr() if y is not None else None, cols,
+    _call(lib().ct_rms_norm_forward, index, px, sx, pr, sr, _dense(weight), y.data_ptr() if y is not None else None, cols,
           h.data_ptr() if h is not None else None, cols, rstd.data_ptr() if rstd is not None else None,
           kept.codes.data_ptr() if kept is not None else None, kept.scales.data_ptr() if kept is not None else None, rows, cols,
           eps, dtype_code(x.dtype), q, group)
@@ -199,6 +215,9 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, wei
     """(dx, dw) of rms_norm from its h and rstd; dresidual is the gradient that
     arrives along h and is added to dx.  Entries not in `need` are None, and dw
     where there is no weight."""
+    if stream is not None:
+        with _on(stream, h):
+            return rms_norm_backward(dy, h, rstd, weight, dresidual, need)
     pd, sd = _rows(dy, h, h.dtype)
     ph, sh = _rows(h)
     pr, sr = _rows(dresidual, h, h.dtype)
@@ -217,7 +236,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, wei
         _check(lib().ct_rms_norm_backward_workspace_bytes(rows, cols, code, ctypes.byref(n)))
         nws = n.value
         ws = torch.empty((nws,), dtype=torch.uint8, device=h.device)
-    _call(lib().ct_rms_norm_backward, index, stream, pd, sd, ph, sh, _dense(rstd), _dense(weight), pr, sr, _dense(dx),
+    _call(lib().ct_rms_norm_backward, index, pd, sd, ph, sh, _dense(rstd), _dense(weight), pr, sr, _dense(dx),
           cols, _dense(dw), _dense(ws), nws, rows, cols, code)
     return dx, dw
 
@@ -250,6 +269,9 @@ def rms_norm_autograd(x, weight=None, residual=None, eps: float = 1e-6):
 
 def checkpoint_store(x: torch.Tensor, quant: str = "int8", group: int = 128, stream=None) -> Checkpoint:
     """x kept in 8 bits, one scale for each `group` values of the last axis."""
+    if stream is not None:
+        with _on(stream, x):
+            return checkpoint_store(x, quant, group)
     q = _quant(quant)
     if q == CT_Q_NONE:
         raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
@@ -257,18 +279,21 @@ def checkpoint_store(x: torch.Tensor, quant: str = "int8", group: int = 128, str
     index = _index_of(x)
     rows, cols = _extent(x)
     c = _new_checkpoint(x, q, group)
-    _call(lib().ct_checkpoint_store, index, stream, px, sx, _dense(c.codes), _dense(c.scales), rows, cols,
+    _call(lib().ct_checkpoint_store, index, px, sx, _dense(c.codes), _dense(c.scales), rows, cols,
           dtype_code(x.dtype), q, group)
     return c
 
 
 def checkpoint_load(c: Checkpoint, dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, in its own dtype or another."""
+    if stream is not None:
+        with _on(stream, c.codes):
+            return checkpoint_load(c, dtype)
     pc, ps = _kept(c)
     index = _index_of(c.codes, c.scales)
     rows, cols = _extent(c.codes)
     y = torch.empty_like(c.codes, dtype=dtype or c.dtype)
-    _call(lib().ct_checkpoint_load, index, stream, pc, ps, y.data_ptr(), cols, rows, cols, dtype_code(y.dtype),
+    _call(lib().ct_checkpoint_load, index, pc, ps, y.data_ptr(), cols, rows, cols, dtype_code(y.dtype),
           _QUANT_OF[c.codes.dtype], c.group)
     return y
 
@@ -277,6 +302,9 @@ def checkpointed_activation(gate: torch.Tensor, up: Optional[torch.Tensor] = Non
                             alpha: float = 0.01, quant: str = "int8", group: int = 128, stream=None):
     """(y, gate checkpoint, up checkpoint): y = act(gate) * up, or act(gate)
     without `up` (whose checkpoint is then None)."""
+    if stream is not None:
+        with _on(stream, gate):
+            return checkpointed_activation(gate, up, activation, alpha, quant, group)
     q, act = _quant(quant), _activation(activation)
     if q == CT_Q_NONE:
         raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
@@ -287,7 +315,7 @@ def checkpointed_activation(gate: torch.Tensor, up: Optional[torch.Tensor] = Non
     y = _like(gate)
     cg = _new_checkpoint(gate, q, group)
     cu = _new_checkpoint(up, q, group) if up is not None else None
-    _call(lib().ct_checkpointed_activation_forward, index, stream, pg, sg, pu, su, y.data_ptr(), cols, cg.codes.data_ptr(),
+    _call(lib().ct_checkpointed_activation_forward, index, pg, sg, pu, su, y.data_ptr(), cols, cg.codes.data_ptr(),
           cg.scales.data_ptr(), cu.codes.data_ptr() if cu else None, cu.scales.data_ptr() if cu else None, rows, cols, act, alpha,
           dtype_code(gate.dtype), q, group)
     return y, cg, cu
@@ -298,6 +326,9 @@ def checkpointed_activation_backward(dy: Optional[torch.Tensor], gate: Checkpoin
     """(dgate, dup) from the checkpoints; with "y" in `need`, (dgate, dup, y),
     y recomputed from them (a following layer's weight gradient reads it).
     Entries not in `need` are None, and dup without `up`."""
+    if stream is not None:
+        with _on(stream, gate.codes):
+            return checkpointed_activation_backward(dy, gate, up, activation, alpha, need)
     act = _activation(activation)
     pg, sg = _kept(gate)
     pu, su = _kept(up, gate.codes)
@@ -312,7 +343,7 @@ def checkpointed_activation_backward(dy: Optional[torch.Tensor], gate: Checkpoin
         return torch.empty_like(gate.codes, dtype=dtype) if name in need else None
 
     dgate, dup, y = new("dgate"), new("dup") if up is not None else None, new("y")
-    _call(lib().ct_checkpointed_activation_backward, index, stream, pd, sd, pg, sg, pu, su, _dense(dgate), cols,
+    _call(lib().ct_checkpointed_activation_backward, index, pd, sd, pg, sg, pu, su, _dense(dgate), cols,
           _dense(dup), cols, _dense(y), cols, rows, cols, act, alpha, dtype_code(dtype), _QUANT_OF[gate.codes.dtype],
           gate.group)
     return (dgate, dup, y) if "y" in need else (dgate, dup)
@@ -405,6 +436,9 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     where given (it may be `state` itself), and is None without "state" in
     `need`.  T = 1 is a streaming step.
     """
+    if stream is not None:
+        with _on(stream, q):
+            return linear_attention(q, k, v, log_decay, state, lengths, scale, state_out, need)
     B, T, H, Dk, Dv = _attention_problem(q, v, log_decay, lengths, state, state_out)
     dt = q.dtype
     pq, sq = _heads(q, (B, T, H, Dk), dt)
@@ -417,7 +451,7 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     code = dtype_code(dt)
     nws = _attention_workspace_bytes(B, T, H, Dk, Dv, code, 0, index)
     ws = torch.empty((nws,), dtype=torch.uint8, device=q.device) if nws else None
-    _call(lib().ct_linear_attention_forward, index, stream, pq, sq, pk, sk, pv, sv, o.data_ptr(),
+    _call(lib().ct_linear_attention_forward, index, pq, sq, pk, sk, pv, sv, o.data_ptr(),
           _strides(T * H * Dv, H * Dv, Dv), _dense(log_decay), _dense(state), _dense(state_out), _dense(lengths),
           _dense(ws), nws, B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
     return o, state_out
@@ -428,6 +462,9 @@ def linear_attention_backward(q, k, v, log_decay, do, state=None, dstate=None, l
     """(dq, dk, dv, dstate) of linear_attention for the gradients `do` of o and
     `dstate` of the last state; the returned dstate is the first state's.
     Entries not in `need` are None, and dstate without `state`."""
+    if stream is not None:
+        with _on(stream, q):
+            return linear_attention_backward(q, k, v, log_decay, do, state, dstate, lengths, scale, need)
     B, T, H, Dk, Dv = _attention_problem(q, v, log_decay, lengths, state, dstate)
     dt = q.dtype
     pq, sq = _heads(q, (B, T, H, Dk), dt)
@@ -448,7 +485,7 @@ def linear_attention_backward(q, k, v, log_decay, do, state=None, dstate=None, l
     code = dtype_code(dt)
     nws = _attention_workspace_bytes(B, T, H, Dk, Dv, code, 1, index)
     ws = torch.empty((nws,), dtype=torch.uint8, device=dev) if nws else None
-    _call(lib().ct_linear_attention_backward, index, stream, pq, sq, pk, sk, pv, sv, po, so, _dense(log_decay),
+    _call(lib().ct_linear_attention_backward, index, pq, sq, pk, sk, pv, sv, po, so, _dense(log_decay),
           _dense(state), _dense(dstate), _dense(lengths), _dense(dq), sqk, _dense(dk), sqk, _dense(dv), svv,
           _dense(dfirst), _dense(ws), nws, B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, code)
     return dq, dk, dv, dfirst
