@@ -787,6 +787,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             }
         if (!STATE && lane == 0) bulk_wait_all();
         __syncwarp();
+        tmem_st_wait();  // stores that a warp which gave up has not waited for
         if constexpr (kHalf)
             if (!(top <= kF16Max)) P.flags[bh] = 1;
     } else if (warp == kLaWorkers) {
@@ -814,12 +815,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 fill(&P.ty, y_full[s], Sh::y(c), DB, t0);
                 ++ny;
             }
-            if (!ok) {
-                // what was issued must land before the CTA exits: the last
-                // fill of each barrier
-                for (int i = max(0, nx - 2); i < nx; ++i) mbar_drain(smem_u32(&x_full[i & 1]), (i >> 1) & 1);
-                for (int i = max(0, ny - 2); i < ny; ++i) mbar_drain(smem_u32(&y_full[i & 1]), (i >> 1) & 1);
-            }
+            // what was issued must land before the CTA exits or makes its
+            // barriers anew: the last fills of each barrier.  Always, as
+            // another warp may give up after the last fill, when no wait of
+            // this one fails any more; on a walk that is done they have landed.
+            for (int i = max(0, nx - 2); i < nx; ++i) mbar_drain(smem_u32(&x_full[i & 1]), (i >> 1) & 1);
+            for (int i = max(0, ny - 2); i < ny; ++i) mbar_drain(smem_u32(&y_full[i & 1]), (i >> 1) & 1);
         }
         __syncwarp();
     } else {
