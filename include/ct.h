@@ -513,7 +513,8 @@ int ct_checkpointed_activation_backward(const void* dy, int64_t dy_stride,
  * [0, T]); o is 0 after them and what q, k and v hold there is not used.
  *   q, k [B, T, H, Dk], v, o [B, T, H, Dv] of one dtype: *_strides give the
  *     element strides of batch, token and head, the last axis is dense.
- *   log_decay [H] fp32, meant to be <= 0 (-infinity: only the token itself).
+ *   log_decay [H] fp32, meant to be <= 0 (-infinity: only the token itself; a
+ *     NaN makes its head NaN).
  *   state_in, state_out [B, H, Dk, Dv] fp32: S before the first and after the
  *     last token; NULL means zero, not wanted.  They may be the same buffer.
  * T = 1 is a streaming step; T = 0 copies state_in.  S and all sums are fp32.

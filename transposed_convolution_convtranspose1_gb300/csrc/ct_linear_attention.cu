@@ -52,8 +52,7 @@ __global__ void __launch_bounds__(kWarps * 32) la_scan(const __grid_constant__ S
     const int n = max(0, min(len, s1) - s0);  // tokens of this segment
     // backward in time the sequence's last token takes the matrix undecayed
     const bool holds_end = A.reverse && n > 0 && s0 + n == len;
-    // exp(0 * g) must be 1 for a decay of zero (g = -infinity) too
-    const float gamma = expf(fmaxf(A.log_decay[h], -1e30f));
+    const float gamma = expf(la_log_decay(A.log_decay[h]));
     const T* z = static_cast<const T*>(A.z) + b * A.zs[0] + s0 * A.zs[1] + h * A.zs[2];
     const T* x = static_cast<const T*>(A.x) + b * A.xs[0] + s0 * A.xs[1] + h * A.xs[2];
     const T* y = static_cast<const T*>(A.y) + b * A.ys[0] + s0 * A.ys[1] + h * A.ys[2];

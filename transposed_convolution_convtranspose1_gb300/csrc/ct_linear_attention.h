@@ -22,6 +22,11 @@ namespace ct {
 
 constexpr int kLaMaxD = 256;  // head sizes
 
+// The logarithm of a decay as the kernels multiply it: a finite one, as
+// exp(0 * g) must be 1 for a decay of zero (g = -infinity) too.  A comparison,
+// not a maximum, so that NaN stays NaN.
+__device__ __forceinline__ float la_log_decay(float g) { return g < -1e30f ? -1e30f : g; }
+
 struct LaCore {
     const void *z, *x, *y;
     void* out;

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             m_out[i] = m_in ? (m_in_t ? m_in[(i % P.Db) * P.Da + i / P.Db] : m_in[i]) : 0.f;
     if (n_chunks > 0) {
 
-    const float g = fmaxf(P.log_decay[h], -1e30f);
+    const float g = la_log_decay(P.log_decay[h]);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&y_full[i]), 1);
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(256) la_chain(const __grid_constant__ LaChainB
     const int bh = (int)(i / msize);
     const int64_t e = i % msize;
     const int len = Q.lengths ? max(0, min(Q.T, Q.lengths[bh / Q.H])) : Q.T;
-    const float g = fmaxf(Q.log_decay[bh % Q.H], -1e30f);
+    const float g = la_log_decay(Q.log_decay[bh % Q.H]);
     float cur = P.m_in ? P.m_in[bh * msize + (P.m_in_t ? (e % P.Db) * P.Da + e / P.Db : e)] : 0.f;
     auto seg_of = [&](int k) { return P.reverse ? Q.segs - 1 - k : k; };
     const int64_t step = (int64_t)Q.BH * msize;
