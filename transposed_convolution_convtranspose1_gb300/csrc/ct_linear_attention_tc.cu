@@ -52,7 +52,10 @@
 // equal runs, one for each SM.  A walk cut by a run's end is begun by the one
 // CTA as its first piece and ended by the next CTA as its last, which takes the
 // matrix from memory; nothing is read twice (the gradients above: 192 walks of
-// 16 chunks, 21 chunks an SM instead of 32; 96 us in two turns).
+// 16 chunks, 21 chunks an SM instead of 32; 96 us in two turns).  CTAs number
+// themselves as they start, so the one that another waits for has started
+// before it, and its first piece waits for nobody: the walks end however many
+// of them the GPU, or the part of it that the stream has, runs at once.
 #include <algorithm>
 #include <cstring>
 
@@ -95,10 +98,11 @@ struct LaTcBatch {
     LaTcParams core[3];
     int ctas;                    // of one core
     // shared walks (quota > 0): the chunks of all walks in a row, cut into runs
-    // of `quota` chunks, one for each CTA of a cooperative launch
+    // of `quota` chunks, one for each CTA
     int quota, chunks, walks;    // chunks: of one walk; quota >= chunks
     float* handed;               // [CTA][Da][Db]
     unsigned* done;              // [CTA]: its first piece's matrix is there
+    unsigned* started;           // CTAs that have taken a number
 };
 
 // Tile n of the walk (Z, X, Y of chunk 0, Z, X, Y of chunk 1, ...) lies in
@@ -328,6 +332,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     __shared__ uint64_t x_full[2], y_full[2], z_free[2], x_free[2], y_free[2];  // x_full: Z and X
     __shared__ uint64_t s_ready, m_ready, a_done, p_done, o_ready, o_free, sum_ready, drain_bar;
     __shared__ uint32_t tmem_slot;
+    __shared__ unsigned number;
     __shared__ volatile int abort_flag;
     // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]:
     // one later, for aligned pairs, half the banks on (lanes take both in turn)
@@ -342,7 +347,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         if (threadIdx.x == 0) atomicOr(&g_device_error, kErrProducer);
         return;
     }
-    if (threadIdx.x == 0) abort_flag = 0;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        number = Q.quota ? atomicAdd(Q.started, 1u) : blockIdx.x;
+    }
     if (warp == kLaWorkers + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
                      : "memory");
@@ -357,10 +365,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     // pieces from its end to its start: the first may be a walk's beginning,
     // handed to the next CTA, the last a walk's end, begun by the CTA before,
     // which had it done before this one's other pieces: quota >= chunks.
-    const int run0 = (int)blockIdx.x * Q.quota;
+    const unsigned me = number;
+    const int run0 = (int)me * Q.quota;
     int run = min(run0 + Q.quota, Q.walks * Q.chunks);
     do {
-    unsigned cta = blockIdx.x;
+    unsigned cta = me;
     int w0 = 0, w1 = 0;  // the piece's chunks of its walk
     if (Q.quota) {
         cta = (unsigned)(run - 1) / (unsigned)Q.chunks;
@@ -393,11 +402,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     }
     const bool begun = w0 > 0, handed = w1 < Q.chunks;  // the CTA before, the next one has the rest
     bool late = false;
-    if (begun && threadIdx.x == 0) late = !wait_done(Q.done + blockIdx.x - 1, P.wait_ns);
+    if (begun && threadIdx.x == 0) late = !wait_done(Q.done + me - 1, P.wait_ns);
     if (__syncthreads_or(late)) break;
-    const float* m_in = begun ? Q.handed + (blockIdx.x - 1) * msize : P.m_in ? P.m_in + (P.m_in_seg ? ((int64_t)seg * P.BH + bh) * msize : bh * msize) : nullptr;
+    const float* m_in = begun ? Q.handed + (me - 1) * msize : P.m_in ? P.m_in + (P.m_in_seg ? ((int64_t)seg * P.BH + bh) * msize : bh * msize) : nullptr;
     const bool m_in_t = P.m_in_t && !begun, last_piece = P.final && !handed;
-    float* m_out = handed ? Q.handed + blockIdx.x * msize : P.m_out ? P.m_out + ((int64_t)seg * P.BH + bh) * msize : nullptr;
+    float* m_out = handed ? Q.handed + me * msize : P.m_out ? P.m_out + ((int64_t)seg * P.BH + bh) * msize : nullptr;
     if (n_chunks == 0 && m_out)  // (the same for every thread)
         for (int64_t i = threadIdx.x; i < msize; i += kLaThreads)
             m_out[i] = m_in ? (m_in_t ? m_in[(i % P.Db) * P.Da + i / P.Db] : m_in[i]) : 0.f;
@@ -929,7 +938,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         }
         if (handed) {  // every thread's part was stored before the barrier above
             __threadfence();
-            asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(Q.done + blockIdx.x), "r"(1u) : "memory");
+            asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(Q.done + me), "r"(1u) : "memory");
         }
     }
     } while (run > run0);
@@ -1000,13 +1009,8 @@ cudaError_t launch_k(const LaTcBatch& Q, int cores, cudaStream_t s) {
     constexpr int bytes = (int)LaShape<DA, DB>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (Q.quota) {  // CTAs that wait for others: all of them on the GPU at once
-        const unsigned grid = (unsigned)(((int64_t)Q.walks * Q.chunks + Q.quota - 1) / Q.quota);
-        LaTcBatch copy = Q;
-        void* args[] = {&copy};
-        return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(k), dim3(grid), dim3(kLaThreads), args, bytes, s);
-    }
-    k<<<(unsigned)(Q.ctas * cores), kLaThreads, bytes, s>>>(Q);
+    const unsigned grid = Q.quota ? (unsigned)(((int64_t)Q.walks * Q.chunks + Q.quota - 1) / Q.quota) : (unsigned)(Q.ctas * cores);
+    k<<<grid, kLaThreads, bytes, s>>>(Q);
     return cudaGetLastError();
 }
 
@@ -1052,7 +1056,7 @@ int share(int64_t walks, int64_t T, int sm_count) {
 }
 
 size_t shared_bytes(int64_t msize, int sm_count) {
-    return round256((size_t)sm_count * msize * sizeof(float)) + round256((size_t)sm_count * sizeof(unsigned));
+    return round256((size_t)sm_count * msize * sizeof(float)) + round256((size_t)(sm_count + 1) * sizeof(unsigned));
 }
 
 size_t core_bytes(int64_t BH, int64_t msize, int segs, int dtype) {
@@ -1175,7 +1179,8 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
         Q.walks = (int)(BH * n);
         Q.handed = reinterpret_cast<float*>(ws);
         Q.done = reinterpret_cast<unsigned*>(ws + round256((size_t)d.sm_count * msize * sizeof(float)));
-        e = cudaMemsetAsync(Q.done, 0, (size_t)d.sm_count * sizeof(unsigned), s);
+        Q.started = Q.done + d.sm_count;
+        e = cudaMemsetAsync(Q.done, 0, (size_t)(d.sm_count + 1) * sizeof(unsigned), s);
         if (e != cudaSuccess) return e;
     }
     if (segs > 1) {
