@@ -518,6 +518,8 @@ int ct_checkpointed_activation_backward(const void* dy, int64_t dy_stride,
  *   state_in, state_out [B, H, Dk, Dv] fp32: S before the first and after the
  *     last token; NULL means zero, not wanted.  They may be the same buffer.
  * T = 1 is a streaming step; T = 0 copies state_in.  S and all sums are fp32.
+ * A value that is not finite reaches what the recurrence takes it to, and no
+ * output of a token before it.
  * Head sizes up to 256.
  * workspace: ct_linear_attention_workspace_bytes bytes (backward: 0 or 1),
  * 256-byte aligned, or NULL (allocated stream-ordered where needed).

@@ -79,6 +79,8 @@ struct LaTcParams {
     CUtensorMap to;              // boxes of DB / 4 columns x 32 tokens
     void* out;
     int64_t os[3];
+    const void *z, *x, *y;       // the same tensors, for la_token_by_token
+    int64_t zs[3], xs[3], ys[3];
     const float* m_in;           // before segment 0 of the walk, or per segment
     int m_in_t, m_in_seg;        // transposed; one for each segment ([seg][bh][Da][Db])
     float* m_out;                // after the walk of a segment ([seg][bh])
@@ -102,6 +104,7 @@ struct LaTcBatch {
     int quota, chunks, walks;    // chunks: of one walk; quota >= chunks
     float* handed;               // [CTA][Da][Db]
     unsigned* done;              // [CTA]: its first piece's matrix is there
+    unsigned* read;              // [CTA]: m_in is not read any more (la_token_by_token)
     unsigned* started;           // CTAs that have taken a number
 };
 
@@ -314,6 +317,114 @@ __device__ __forceinline__ bool wait_done(const unsigned* done, uint64_t limit_n
     }
 }
 
+// Votes of the worker warps (a barrier of theirs).
+__device__ __forceinline__ bool workers_any(bool v) {
+    unsigned r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, 1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((unsigned)v), "n"(kLaWorkers * 32)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool not_finite(float v) { return !(fabsf(v) < __uint_as_float(0x7f800000u)); }
+__device__ __forceinline__ void set_done(unsigned* done) {
+    __threadfence();
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(done), "r"(1u) : "memory");
+}
+
+// Pieces of this CTA's run once more (bit i: of the i-th walk it meets), token
+// by token, M in shared memory (`M`, 128 columns a row, then the token's
+// values).  In a chunk's products a row meets every token's y with a factor of
+// 0 where it does not see it, and 0 times an infinity or a NaN is NaN: outputs
+// of tokens before such a value are lost with the others.  Here no token meets
+// a later one.  For pieces that hold such values alone, and after everything
+// else, so that nothing of it is alive in the walk's own loop.
+//
+// A walk's last matrix may take the first one's place.  The CTA that ends such
+// a walk leaves it to this function, and waits until the CTA that began the
+// walk has read the first one again: pieces that begin a walk come first here
+// and wait for nobody.
+template <typename T>
+__device__ __forceinline__ void la_token_by_token(const LaTcBatch& Q, unsigned me, unsigned pieces, float* M) {
+    float *xs = M + 128 * 128, *zs = xs + 128, *ys = zs + 128, *part = ys + 128;
+    const int tid = threadIdx.x, c = tid & 127, quarter = tid >> 7;
+    const int run0 = (int)me * Q.quota, run1 = min(run0 + Q.quota, Q.walks * Q.chunks);
+#pragma unroll 1
+    while (pieces) {
+        const int piece = 31 - __clz(pieces);
+        pieces ^= 1u << piece;
+        unsigned cta = me;
+        int w0 = 0, w1 = Q.chunks;  // (no quota: 0 chunks)
+        if (Q.quota) {
+            cta = run0 / Q.chunks + piece;
+            w0 = max(run0 - (int)cta * Q.chunks, 0);
+            w1 = min(run1 - (int)cta * Q.chunks, Q.chunks);
+        }
+        const bool begun = w0 > 0, handed = w1 < Q.chunks;
+        const LaTcParams& P = Q.core[cta / (unsigned)Q.ctas];
+        cta %= (unsigned)Q.ctas;
+        const int bh = (int)(cta % (unsigned)P.BH), seg = (int)(cta / (unsigned)P.BH), b = bh / P.H, h = bh % P.H;
+        const int len = P.lengths ? max(0, min(P.T, P.lengths[b])) : P.T;
+        const int s0 = Q.quota ? (P.reverse ? Q.chunks - w1 : w0) * kC : seg * P.seg_tokens;
+        const int s1 = min(P.T, Q.quota ? s0 + (w1 - w0) * kC : s0 + P.seg_tokens);
+        const int n = max(0, min(len, s1) - s0);
+        const bool holds_end = P.reverse && s0 + n == len;
+        const int64_t msize = (int64_t)P.Da * P.Db;
+        const float* m_in = begun ? Q.handed + (me - 1) * msize : P.m_in ? P.m_in + ((P.m_in_seg ? (int64_t)seg * P.BH : 0) + bh) * msize : nullptr;
+        const bool m_in_t = P.m_in_t && !begun;
+        const float gamma = expf(la_log_decay(P.log_decay[h]));
+        const int a0 = quarter * 32, a1 = min(a0 + 32, P.Da);
+        bool odd = false;
+        if (c < P.Db)
+#pragma unroll 1
+            for (int a = a0; a < a1; ++a) {
+                const float m = m_in ? m_in[m_in_t ? (int64_t)c * P.Da + a : (int64_t)a * P.Db + c] : 0.f;
+                M[a * 128 + c] = m;
+                odd = odd || not_finite(m);
+            }
+        odd = workers_any(odd);
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            const int64_t t = s0 + (P.reverse ? n - 1 - k : k);
+            if (quarter == 0 && c < P.Da) xs[c] = to_f32(static_cast<const T*>(P.x)[b * P.xs[0] + t * P.xs[1] + h * P.xs[2] + c]) * P.mscale;
+            if (quarter == 1 && c < P.Da) zs[c] = to_f32(static_cast<const T*>(P.z)[b * P.zs[0] + t * P.zs[1] + h * P.zs[2] + c]);
+            if (quarter == 2 && c < P.Db) ys[c] = to_f32(static_cast<const T*>(P.y)[b * P.ys[0] + t * P.ys[1] + h * P.ys[2] + c]);
+            workers_any(false);
+            const float g = holds_end && k == 0 ? 1.f : gamma;
+            float sum = 0.f;
+            if (c < P.Db)
+#pragma unroll 4
+                for (int a = a0; a < a1; ++a) {
+                    const float m = fmaf(xs[a], ys[c], g * M[a * 128 + c]);
+                    M[a * 128 + c] = m;
+                    sum = fmaf(m, zs[a], sum);
+                }
+            part[tid] = sum;
+            workers_any(false);
+            if (tid < P.Db)
+                static_cast<T*>(P.out)[b * P.os[0] + t * P.os[1] + h * P.os[2] + tid] =
+                    from_f32<T>((part[tid] + part[128 + tid] + part[256 + tid] + part[384 + tid]) * P.oscale);
+        }
+        if (handed) {  // its matrix is where the next CTA takes it
+            if (tid == 0) set_done(Q.read + me);
+        } else if (P.m_out && P.final) {
+            // the matrix began so: the CTA before is at its piece once more
+            if (begun && odd && P.m_out == P.m_in) {
+                const bool late = tid == 0 && !wait_done(Q.read + me - 1, P.wait_ns);
+                if (workers_any(late)) return;
+            }
+            const float last = P.reverse && n > 0 ? gamma : 1.f;
+            if (c < P.Db)
+#pragma unroll 1
+                for (int a = a0; a < a1; ++a) P.m_out[bh * msize + (int64_t)a * P.Db + c] = M[a * 128 + c] * last;
+        }
+    }
+}
+
 template <typename T, int DA, int DB, bool STATE>
 __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcBatch Q) {
     using Sh = LaShape<DA, DB>;
@@ -334,6 +445,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     __shared__ uint32_t tmem_slot;
     __shared__ unsigned number;
     __shared__ volatile int abort_flag;
+    __shared__ unsigned again;  // pieces for la_token_by_token
     // tab[0][kC - 1 + j - i]: factor of S[i][j], 0 where i does not see j; [1]:
     // one later, for aligned pairs, half the banks on (lanes take both in turn)
     __shared__ __align__(8) float tab[2][2 * kC + 16];
@@ -349,6 +461,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     }
     if (threadIdx.x == 0) {
         abort_flag = 0;
+        again = 0;
         number = Q.quota ? atomicAdd(Q.started, 1u) : blockIdx.x;
     }
     if (warp == kLaWorkers + 1) {
@@ -771,7 +884,17 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 }
             }
         }
-        if (ok && m_out && row < P.Da) {
+        // What is not finite in x or y leaves its trace in M: then the outputs
+        // are formed once more (also those of a walk whose M began so).
+        bool once_more = false;
+        if constexpr (!STATE) {
+            float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kN; i += 2) t = __ffma2_rn(make_float2(mv[i], mv[i + 1]), make_float2(0.f, 0.f), t);
+            once_more = workers_any(row < P.Da && !(t.x + t.y == 0.f));
+            if (once_more && threadIdx.x == 0) again |= Q.quota ? 1u << (run / Q.chunks - run0 / Q.chunks) : 1u;
+        }
+        if (ok && m_out && row < P.Da && (!once_more || handed)) {  // (m_in may be m_out, and is read once more)
             const float last = P.reverse && last_piece ? pw[1] : 1.f;
 #pragma unroll
             for (int i = 0; i < kN; ++i) mv[i] *= last;
@@ -936,10 +1059,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             mbar_inval(smem_u32(&sum_ready));
             mbar_inval(smem_u32(&drain_bar));
         }
-        if (handed) {  // every thread's part was stored before the barrier above
-            __threadfence();
-            asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(Q.done + me), "r"(1u) : "memory");
-        }
+        if (handed) set_done(Q.done + me);  // every thread's part was stored before the barrier above
     }
     } while (run > run0);
 
@@ -948,6 +1068,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
     tc_fence_after();
     if (warp == kLaWorkers + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if constexpr (!STATE)
+        if (again && !abort_flag && warp < kLaWorkers) la_token_by_token<T>(Q, number, again, reinterpret_cast<float*>(smem_raw));
 }
 
 // cur <- decay^n cur + sum, element by element along the walk.
@@ -1056,7 +1178,7 @@ int share(int64_t walks, int64_t T, int sm_count) {
 }
 
 size_t shared_bytes(int64_t msize, int sm_count) {
-    return round256((size_t)sm_count * msize * sizeof(float)) + round256((size_t)(sm_count + 1) * sizeof(unsigned));
+    return round256((size_t)sm_count * msize * sizeof(float)) + round256((size_t)(2 * sm_count + 1) * sizeof(unsigned));
 }
 
 size_t core_bytes(int64_t BH, int64_t msize, int segs, int dtype) {
@@ -1145,7 +1267,15 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
             if (e != cudaSuccess) return e;
         }
         P.out = c.out;
-        for (int k = 0; k < 3; ++k) P.os[k] = c.os[k];
+        P.z = c.z;
+        P.x = c.x;
+        P.y = c.y;
+        for (int k = 0; k < 3; ++k) {
+            P.os[k] = c.os[k];
+            P.zs[k] = c.zs[k];
+            P.xs[k] = c.xs[k];
+            P.ys[k] = c.ys[k];
+        }
         P.log_decay = c.log_decay;
         P.lengths = c.lengths;
         P.flags = flags[i];
@@ -1179,8 +1309,9 @@ cudaError_t launch_la_tc(const LaCore* cores, int n, void* workspace, cudaStream
         Q.walks = (int)(BH * n);
         Q.handed = reinterpret_cast<float*>(ws);
         Q.done = reinterpret_cast<unsigned*>(ws + round256((size_t)d.sm_count * msize * sizeof(float)));
-        Q.started = Q.done + d.sm_count;
-        e = cudaMemsetAsync(Q.done, 0, (size_t)(d.sm_count + 1) * sizeof(unsigned), s);
+        Q.read = Q.done + d.sm_count;
+        Q.started = Q.read + d.sm_count;
+        e = cudaMemsetAsync(Q.done, 0, (size_t)(2 * d.sm_count + 1) * sizeof(unsigned), s);
         if (e != cudaSuccess) return e;
     }
     if (segs > 1) {
