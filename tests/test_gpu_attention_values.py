@@ -1,4 +1,4 @@
-"""Linear attention on values at the ends: decays that are NaN, infinities and NaN among the values."""
+"""Linear attention on values at the ends: decays that are NaN, infinities and NaN among the values, small fp16 values."""
 import pytest
 import torch
 
@@ -106,3 +106,35 @@ def test_what_is_not_finite_reaches_only_those_who_see_it(dtype, where, Dk, Dv):
             assert not wrong.any(), f"{what}: {wrong.sum().item()} of {wrong.numel()} finite or not in the wrong place"
             off = ((g.double() - r).abs() - (r.abs() * u + m * kk + tiny))[fine]
             assert off.max().item() <= 0, f"{what}: {off.max().item():.3e} over its bound"
+
+
+# ---- small fp16 values -----------------------------------------------------------
+
+def off(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (64, 128)])
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-5, 3e-6])
+@pytest.mark.parametrize("small", ["do", "k and v", "state"])
+def test_small_fp16_values_keep_their_digits(Dk, Dv, size, small):
+    """Gradients of the sizes that a mean loss gives, small keys and values, a small state read by large queries: no output is
+    further from 64 bits than rounding it to fp16 and 2^-17 of its terms come to."""
+    B, T, H = 2, 300, 2
+    q, k, v, do, ld, s, ds = inputs(Dk + Dv, B, T, H, Dk, Dv, "f16")
+    ld = -torch.tensor([1.0 / 128, 1.0 / 16], device="cuda")
+    if small == "do":
+        do, s, ds = do * size, None, None
+    elif small == "k and v":
+        k, v, s, ds = k * size ** 0.5, v * size ** 0.5, s * size, None
+    else:
+        q, k, v, s, ds = q * 64, k * size, v * size, s * size, None
+    got = outputs(q, k, v, ld, do, s, ds)
+    for name, i, j, walk in walks(q, k, v, ld, do, s, ds, None, Dk ** -0.5):
+        (ref, refm), (mag, magm) = reference(ld, walk)
+        rounded = off(ref.half(), ref)
+        limit = 1.05 * rounded + 2.0 ** -17 * (mag.norm() / ref.norm()).item()
+        assert off(got[i], ref) <= limit, f"{name}: {off(got[i], ref):.2e}, rounding alone {rounded:.2e}, limit {limit:.2e}"
+        if j is not None and got[j] is not None:
+            limit = 2.0 ** -17 * (magm.norm() / refm.norm()).item()
+            assert off(got[j], refm) <= limit, f"{name} state: {off(got[j], refm):.2e}, limit {limit:.2e}"

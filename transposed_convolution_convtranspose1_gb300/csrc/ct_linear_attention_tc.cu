@@ -18,8 +18,11 @@
 // one rounding each, out's error would be 1.4 to 1.7 times that of rounding
 // out itself, and the fp32 state's 2^-9; with two, both to nearest, a bf16
 // value keeps about 17 bits (an f16 one 22) and the state comes to about 3e-6
-// of its norm.  P and x enter from TMEM (P over S,
-// in place), M from shared memory.
+// of its norm.  f16's lo parts are kept 2^11 times their size, or they would
+// lose their digits where values are small (gradients of 1e-5 came out 1e-3
+// off, a state of 1e-6 under queries of 64 8e-3): their products are summed
+// first, and the MMA that adds the first of the others scales the sum down.
+// P and x enter from TMEM (P over S, in place), M from shared memory.
 //
 // One CTA per sequence, head and segment walks its chunks in order.  Sixteen
 // warps do the same step of the work at the same time, each a lane quarter of
@@ -153,6 +156,27 @@ __device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint64_t a_desc, uin
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same with D scaled by 2^-DOWN before the product is added.
+template <int DOWN>
+__device__ __forceinline__ void mma_ss_down(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p, %4;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(DOWN)
+        : "memory");
+}
+template <int DOWN>
+__device__ __forceinline__ void mma_ts_down(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %4;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "n"(DOWN)
+        : "memory");
+}
 // D += A B with A (16-bit, two consecutive K in a column) in TMEM.
 __device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
     asm volatile(
@@ -283,11 +307,19 @@ template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
 template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-// v = hi + lo to within U^2 |v|, each half a T.
+// v = hi + lo / kLoUp to within U^2 |v|, each half a T.  f16 has five bits of
+// exponent: lo is kept 2^11 times its size, as large as hi, so that it has all
+// its digits wherever hi has (and the sum is good to 2^-36 below that, where hi
+// is subnormal).
+template <typename T>
+constexpr int kLoBits = std::is_same<T, __half>::value ? 11 : 0;
+template <typename T>
+constexpr float kLoUp = (float)(1 << kLoBits<T>);
 template <typename T>
 __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
     hi = pack2<T>(v.x, v.y);
-    const float2 r = __ffma2_rn(unpack2<T>(hi), make_float2(-1.f, -1.f), v);
+    float2 r = __ffma2_rn(unpack2<T>(hi), make_float2(-1.f, -1.f), v);
+    if constexpr (kLoBits<T> != 0) r = __fmul2_rn(r, make_float2(kLoUp<T>, kLoUp<T>));
     lo = pack2<T>(r.x, r.y);
 }
 
@@ -429,12 +461,13 @@ template <typename T, int DA, int DB, bool STATE>
 __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant__ LaTcBatch Q) {
     using Sh = LaShape<DA, DB>;
     constexpr bool kHalf = std::is_same<T, __half>::value;
-    // f16 scores and decayed x are kept 16 and 64 times their size: the lo
-    // parts' steps then are 2^-28 and 2^-30, the ranges 4094 and 1023; beyond
-    // them the flag has the head done again
+    // f16 scores and decayed x are kept 16 and 64 times their size: the ranges
+    // then are 4094 and 1023 (beyond them the flag has the head done again),
+    // and they are good to 2^-40 and 2^-42 where they are smallest, M to 2^-36
     constexpr float kUp = kHalf ? 16.f : 1.f, kUpX = kHalf ? 64.f : 1.f;
     constexpr int kN = DB / 4;  // columns of Y, M and out a warp has
     constexpr bool kStacked = Sh::kStacked;
+    constexpr int kDown = kLoBits<T>;
     // 64 columns of out and M leave room for a second S: the next chunk's is
     // formed before P Y of this one
     constexpr bool kTwoS = DB == 64;
@@ -572,6 +605,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         const int row = w4 * 32 + lane, col0 = g4 * kN;
         const bool fed = DA == 128 || kStacked || w4 * 32 < DA;  // columns of X feed this lane quarter of the decayed x and of M
         [[maybe_unused]] float top = 0.f;
+        // TMEM's M times its true size: stacked, the sums of lo products keep
+        // lo's scale; otherwise M starts a chunk in it, as lo products come
+        // first, and ends in hi's
+        const bool lo_rows = kStacked && w4 >= 2;
+        const float m_start = !kStacked || lo_rows ? kUpX * kLoUp<T> : kUpX, m_end = lo_rows ? 1.f / (kUpX * kLoUp<T>) : 1.f / kUpX;
         bool ok = true;
         if (!fed) {
             uint32_t zero[32];
@@ -678,7 +716,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         auto rescale = [&] {  // what TMEM holds to M
             if constexpr (kHalf)
 #pragma unroll
-                for (int i = 0; i < kN; ++i) mv[i] *= 1.f / kUpX;
+                for (int i = 0; i < kN; ++i) mv[i] *= m_end;
         };
         for (int c = 0; c < n_chunks; ++c) {
             const int n = rows_of(chunk_at(c));
@@ -689,7 +727,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
             ok = !STATE && kTwoS ? waits(s_ready, c, kErrEpilogue) : waits(x_full[c & 1], c >> 1, kErrEpilogue);
             if (!ok) break;
             if constexpr (kStacked) {
-                if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
+                if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * m_start);
                 // 8 columns of a token at a time, in the tile's own places, the
                 // second ones loaded before the first are split
                 const int j0 = threadIdx.x >> 3;
@@ -736,7 +774,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                         ldsm4_trans(xs + Sh::x(c) + k * 2048u + (((ch + ah * 2) ^ (lane & 7)) << 4), x[ah] + 4 * k);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) f[m] = ft[4 * m];
-                if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
+                if (!STATE) tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * m_start);
                 if constexpr (kUpX != kUp)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) f[m] = __fmul2_rn(f[m], make_float2(kUpX / kUp, kUpX / kUp));
@@ -767,7 +805,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     tmem_ld_wait();
                     rescale();
                 }
-                tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * kUpX);
+                tmem_st_scaled<kN>(lane_base + kTmemM + col0, mv, pw[n - first] * m_start);
                 tmem_st_wait();
             }
             if (n < kC) {  // rows of Y after the end meet factors of 0: they must be finite
@@ -791,12 +829,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 m = make_float2(mv[8 * k + 2 * i], mv[8 * k + 2 * i + 1]);
+                            float2 m = make_float2(mv[8 * k + 2 * i], mv[8 * k + 2 * i + 1]);
+                            if constexpr (kStacked && kHalf)
+                                if (lo_rows) m = __fmul2_rn(m, make_float2(kLoUp<T>, kLoUp<T>));
                             split2<T>(m, hi[i], lo[i]);
                             if constexpr (kHalf) top = fmaxf(top, fmaxf(fabsf(m.x), fabsf(m.y)));
                         }
                         const uint32_t o = ((uint32_t)(((col0 & 63) >> 3) + k) ^ (uint32_t)(row & 7)) * 16u;
-                        if (kStacked && w4 >= 2) {  // the sum of lo products: 2^-9 of M, its hi part is enough
+                        if (lo_rows) {  // 2^-9 (2^-12) of M: their hi part is enough
                             sts128(at + 2 * Sh::kM + o, hi[0], hi[1], hi[2], hi[3]);
                             continue;
                         }
@@ -841,7 +881,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                     tmem_ldn<kN>(lane_base + kTmemM + col0, mv);
                     tmem_ld_wait();
                     // rows after the end may hold NaN; they are not stored
-                    tmem_st_scaled<kN>(lane_base + kTmemO + col0, v, row < n ? pw[w] * kUp : 0.f);
+                    tmem_st_scaled<kN>(lane_base + kTmemO + col0, v, row < n ? pw[w] * (kUp * kLoUp<T>) : 0.f);
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -959,14 +999,23 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
         // ------------------------------------------------------- MMA issue
         // the whole warp walks and waits; one elected lane issues
         auto wait1 = [&](uint64_t& bar, int parity) { return waits(bar, parity, kErrMma); };
-        // D += A B over the chunk's tokens, A = hi + lo in TMEM
+        // D += A B over the chunk's tokens, A = hi + lo in TMEM.  f16: D comes
+        // in lo's scale, takes the lo products and then, scaled down, the others
         auto by_y = [&](uint32_t d, uint32_t at, int c) {
             const uint64_t yd = desc_mn(base + Sh::y(c), 16384);
+            auto ad = [&](int k) { return at + (k / 2) * 32 + (k & 1) * 8; };
+            if constexpr (kDown == 0) {
 #pragma unroll
-            for (int k = 0; k < kC / 16; ++k) {
-                const uint32_t ad = at + (k / 2) * 32 + (k & 1) * 8;
-                mma_ts_one(d, ad, yd + 128 * k, P.idesc_n);
-                mma_ts_one(d, ad + 16, yd + 128 * k, P.idesc_n);
+                for (int k = 0; k < kC / 16; ++k) {
+                    mma_ts_one(d, ad(k), yd + 128 * k, P.idesc_n);
+                    mma_ts_one(d, ad(k) + 16, yd + 128 * k, P.idesc_n);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k) mma_ts_one(d, ad(k) + 16, yd + 128 * k, P.idesc_n);
+                mma_ts_down<kDown>(d, ad(0), yd, P.idesc_n);
+#pragma unroll
+                for (int k = 1; k < kC / 16; ++k) mma_ts_one(d, ad(k), yd + 128 * k, P.idesc_n);
             }
         };
         auto form_s = [&](int c) {  // false where a wait gave up
@@ -1004,12 +1053,23 @@ __global__ void __launch_bounds__(kLaThreads, 1) la_chunks(const __grid_constant
                 tc_fence_after();
                 const uint64_t zd = smem_desc_sw128(base + Sh::z(c));
                 const uint64_t mh = desc_mn(base + Sh::oM, DA * 128), ml = desc_mn(base + Sh::oM + Sh::kM, DA * 128);
+                auto zo = [&](int k) { return zd + (k / 4) * 1024 + (k & 3) * 2; };
+                if constexpr (kDown == 0) {
 #pragma unroll
-                for (int k = 0; k < DA / 16; ++k) {
-                    const uint32_t o = (k / 4) * 1024 + (k & 3) * 2;
-                    mma_ss_one(tmem + kTmemO, zd + o, mh + 128 * k, P.idesc_n, k > 0);
-                    mma_ss_one(tmem + kTmemO, zd + o, ml + 128 * k, P.idesc_n, 1);
-                    if constexpr (kStacked) mma_ss_one(tmem + kTmemO, zd + o, ml + (Sh::kM >> 4) + 128 * k, P.idesc_n, 1);
+                    for (int k = 0; k < DA / 16; ++k) {
+                        mma_ss_one(tmem + kTmemO, zo(k), mh + 128 * k, P.idesc_n, k > 0);
+                        mma_ss_one(tmem + kTmemO, zo(k), ml + 128 * k, P.idesc_n, 1);
+                        if constexpr (kStacked) mma_ss_one(tmem + kTmemO, zo(k), ml + (Sh::kM >> 4) + 128 * k, P.idesc_n, 1);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < DA / 16; ++k) {
+                        mma_ss_one(tmem + kTmemO, zo(k), ml + 128 * k, P.idesc_n, k > 0);
+                        if constexpr (kStacked) mma_ss_one(tmem + kTmemO, zo(k), ml + (Sh::kM >> 4) + 128 * k, P.idesc_n, 1);
+                    }
+                    mma_ss_down<kDown>(tmem + kTmemO, zo(0), mh, P.idesc_n);
+#pragma unroll
+                    for (int k = 1; k < DA / 16; ++k) mma_ss_one(tmem + kTmemO, zo(k), mh + 128 * k, P.idesc_n, 1);
                 }
                 commit_one(z_free[s]);
                 commit_one(m_ready);  // the new M and Z M
