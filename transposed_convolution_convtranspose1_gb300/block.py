@@ -510,5 +510,10 @@ class LinearAttentionFunction(torch.autograd.Function):
 
 
 def linear_attention_autograd(q, k, v, log_decay, state=None, lengths=None, scale: Optional[float] = None):
-    """linear_attention that records itself for torch.autograd; returns (o, state)."""
+    """linear_attention that records itself for torch.autograd; returns (o, state).
+
+    The decays are constants: a log_decay that asks for a gradient is refused
+    (it would get none); pass log_decay.detach()."""
+    if log_decay.requires_grad and torch.is_grad_enabled():
+        raise CtError(CT_ERR_PARAM, "log_decay gets no gradient: pass log_decay.detach()")
     return LinearAttentionFunction.apply(q, k, v, log_decay, state, lengths, scale)
