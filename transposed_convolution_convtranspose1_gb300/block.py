@@ -14,6 +14,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .ct import (ACTIVATIONS, CT_ERR_DTYPE, CT_ERR_PARAM, CT_ERR_SHAPE, CtError, _check, _stream_handle,
                  dtype_code, lib)
@@ -252,6 +253,7 @@ class RmsNormFunction(torch.autograd.Function):
         return (y, h) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, rstd, weight = ctx.saved_tensors
         need = tuple(n for n, flag in (("dx", ctx.needs_input_grad[0] or ctx.needs_input_grad[2]),
@@ -360,6 +362,7 @@ class CheckpointedActivationFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         activation, alpha, group, dtype = ctx.args
         t = ctx.saved_tensors
@@ -501,6 +504,7 @@ class LinearAttentionFunction(torch.autograd.Function):
         return linear_attention(q, k, v, log_decay, state, lengths, scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dstate):
         q, k, v, log_decay, state, lengths = ctx.saved_tensors
         need = tuple(n for n, i in (("dq", 0), ("dk", 1), ("dv", 2), ("dstate", 4)) if ctx.needs_input_grad[i])

@@ -13,6 +13,7 @@ import threading
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libct.so")
@@ -534,6 +535,7 @@ class ConvTransposeFunction(torch.autograd.Function):
                               output_padding, groups)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         stride, padding, pad_lo, pad_hi, dilation, output_padding, groups = ctx.attrs
         need = tuple(n for n, flag in (("dx", ctx.needs_input_grad[0]),
