@@ -38,3 +38,22 @@ def test_a_second_derivative_is_refused(name):
         loss.backward(retain_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (loss + grad.square().sum()).backward(retain_graph=True)
+
+
+@pytest.mark.parametrize("quant", ["int8", "e4m3"])
+@pytest.mark.parametrize("positions", [4, 300])
+def test_what_the_convolution_keeps(positions, quant):
+    """8-bit codes and a scale for each 128 positions of a channel where dw is asked for, nothing of x where it is not."""
+    g = gen(3)
+    x, w = randn(g, 3, 16, positions, dtype="bf16"), randn(g, 16, 8, 4, dtype="bf16")
+    dy = randn(g, 3, 8, 2 * positions, dtype="bf16")
+    grads = {}
+    for dw in (True, False):
+        leaf, weight = x.clone().requires_grad_(), w.clone().requires_grad_(dw)
+        y = ct.conv_transpose_autograd(leaf, weight, stride=2, padding=1, checkpoint=quant)
+        kept = [t for t in y.grad_fn.saved_tensors if t is not None and t.data_ptr() != weight.data_ptr()]
+        assert sum(t.numel() * t.element_size() for t in kept) == (3 * 16 * (positions + 4 * -(-positions // 128)) if dw else 0)
+        y.backward(dy)
+        grads[dw] = leaf.grad
+        assert (weight.grad is not None) == dw
+    assert torch.equal(grads[True], grads[False])

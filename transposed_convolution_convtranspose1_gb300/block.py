@@ -140,6 +140,13 @@ def _quant(quant) -> int:
     return QUANTS[quant]
 
 
+def _checkpoint_quant(quant) -> int:
+    q = _quant(quant)
+    if q == CT_Q_NONE:
+        raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
+    return q
+
+
 def _activation(a) -> int:
     if isinstance(a, str):
         if a not in ACTIVATIONS:
@@ -274,9 +281,7 @@ def checkpoint_store(x: torch.Tensor, quant: str = "int8", group: int = 128, str
     if stream is not None:
         with _on(stream, x):
             return checkpoint_store(x, quant, group)
-    q = _quant(quant)
-    if q == CT_Q_NONE:
-        raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
+    q = _checkpoint_quant(quant)
     px, sx = _rows(x)
     index = _index_of(x)
     rows, cols = _extent(x)
@@ -307,9 +312,7 @@ def checkpointed_activation(gate: torch.Tensor, up: Optional[torch.Tensor] = Non
     if stream is not None:
         with _on(stream, gate):
             return checkpointed_activation(gate, up, activation, alpha, quant, group)
-    q, act = _quant(quant), _activation(activation)
-    if q == CT_Q_NONE:
-        raise CtError(CT_ERR_PARAM, "a checkpoint is 'int8' or 'e4m3'")
+    q, act = _checkpoint_quant(quant), _activation(activation)
     pg, sg = _rows(gate)
     pu, su = _rows(up, gate, gate.dtype)
     index = _index_of(gate, up)
