@@ -224,8 +224,10 @@ cudaError_t launch(const ScanArgs& S, int segs, cudaStream_t s) {
 // of 256 tokens 40 and 41; 15 heads of 40 x 72, 333 tokens in five 41, in one
 // 78).
 void scan_split(int64_t BH, int64_t T, int64_t Db, int* segs, int* tokens) {
+    DeviceInfo d;
+    const int64_t room = 2 * (device_info(&d) == cudaSuccess ? d.sm_count : 152);
     const int64_t blocks = std::max<int64_t>(1, BH * ((Db + kCols - 1) / kCols));
-    int64_t want = std::min<int64_t>(std::min<int64_t>(304 / blocks, T / 64), 4096);
+    int64_t want = std::min<int64_t>(std::min<int64_t>(room / blocks, T / 64), 4096);
     if (want < 4) want = 1;
     *tokens = (int)std::max<int64_t>(1, (T + want - 1) / want);
     *segs = (int)std::max<int64_t>(1, (T + *tokens - 1) / *tokens);
