@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_phase_gemm(const __grid_consta
                         }
             }
         }
-        if (!ok && lane == 0) {
-            // every copy issued so far must land before the CTA exits
+        if (lane == 0) {
+            // every copy issued must land before the CTA exits, also where
+            // another role gives up after the last of them
             const uint32_t first = issued > (uint32_t)P.stages ? issued - P.stages : 0;
             for (uint32_t k = first; k < issued; ++k)
                 mbar_drain(smem_u32(&full_bar[k % P.stages]), (k / P.stages) & 1);
@@ -808,7 +809,9 @@ __global__ void __launch_bounds__(kDwThreads, 1) tc_dw_gemm(const __grid_constan
                 phase ^= 1;
             }
         }
-        if (!ok && lane == 0) {
+        if (lane == 0) {
+            // every copy issued must land before the CTA exits, also where
+            // another role gives up after the last of them
             const uint32_t first = issued > (uint32_t)P.stages ? issued - P.stages : 0;
             for (uint32_t k = first; k < issued; ++k)
                 mbar_drain(smem_u32(&full_bar[k % P.stages]), (k / P.stages) & 1);
