@@ -517,7 +517,11 @@ int ct_checkpointed_activation_backward(const void* dy, int64_t dy_stride,
  *     NaN makes its head NaN).
  *   state_in, state_out [B, H, Dk, Dv] fp32: S before the first and after the
  *     last token; NULL means zero, not wanted.  They may be the same buffer.
- * T = 1 is a streaming step; T = 0 copies state_in.  S and all sums are fp32.
+ * T = 1 is a streaming step; T = 0 copies state_in.  S and all sums are fp32;
+ * where 16-bit types go through the tensor cores (T > 32, head sizes up to 128)
+ * an operand that is not a 16-bit number itself enters as a sum of two, which
+ * leaves the last state good to 4e-6 of its size for bf16 and 4e-7 for fp16
+ * (fp32: 6e-7).
  * A value that is not finite reaches what the recurrence takes it to, and no
  * output of a token before it.
  * Head sizes up to 256.

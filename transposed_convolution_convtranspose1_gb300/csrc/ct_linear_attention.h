@@ -62,9 +62,11 @@ struct LaChainBatch {
 cudaError_t launch_la_chain(const LaChainBatch& c, int n, cudaStream_t stream);
 
 // Sequences of at most this many tokens go token by token.  A chunk costs the
-// same for 33 tokens as for 128, a scan grows by the token (bf16, 64 heads, us
-// with the call: of 64, chunks / scan 20.4 / 18.9 at 33 tokens, 21.4 / 23.7 at
-// 96; of 128, 21.3 / 19.0 at 33, 21.0 / 23.0 at 48).
+// same for 33 tokens as for 128, a scan grows by the token (bf16, us on the
+// GPU, scan / chunks: 64 heads of 64, 9.9 / 10.6 at 32 tokens, 12.8 / 11.0 at
+// 48; of 128, 13.4 / 14.7 at 24, 15.9 / 14.3 at 32; 512 heads, several turns of
+// chunks: of 64, 23.8 / 40.1 at 32, 40.4 / 40.3 at 64; of 128, 41.8 / 54.6 at
+// 16, 69.8 / 57.2 at 24).
 constexpr int kLaScanTokens = 32;
 
 // Token by token on CUDA cores, the matrix in registers

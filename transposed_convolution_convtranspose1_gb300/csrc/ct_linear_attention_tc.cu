@@ -43,8 +43,8 @@
 // would take 5650 (4 x 128 x D x 2 bytes at the SM's share of the copy rate)
 // and 2820, the MMAs 3600 at D = 128.  Measured: 8 x 2048 x 16 heads of 128
 // with the last state 67 us (61% of the copy rate), 32768 tokens of 8
-// heads of 64 in 19 segments 90 us, the three gradients of 8 x 2048 x 8 heads
-// of 64 in one launch 80 us.
+// heads of 64 in 19 segments 91 us, the three gradients of 8 x 2048 x 8 heads
+// of 64 in one launch 78 us.
 //
 // Few heads and long sequences: a sequence is cut into segments.  A first
 // launch forms each segment's own sum (the last line above from M = 0), a
@@ -373,8 +373,10 @@ __device__ __forceinline__ void set_done(unsigned* done) {
 // values).  In a chunk's products a row meets every token's y with a factor of
 // 0 where it does not see it, and 0 times an infinity or a NaN is NaN: outputs
 // of tokens before such a value are lost with the others.  Here no token meets
-// a later one.  For pieces that hold such values alone, and after everything
-// else, so that nothing of it is alive in the walk's own loop.
+// a later one.  For pieces that hold such values alone (2 us a token), and
+// after everything else, so that nothing of it is alive in the walk's own loop
+// (M in registers takes half the time here, but 2 us of each of the three cases
+// above).
 //
 // A walk's last matrix may take the first one's place.  The CTA that ends such
 // a walk leaves it to this function, and waits until the CTA that began the
