@@ -375,8 +375,8 @@ __device__ __forceinline__ void set_done(unsigned* done) {
 // of tokens before such a value are lost with the others.  Here no token meets
 // a later one.  For pieces that hold such values alone (2 us a token), and
 // after everything else, so that nothing of it is alive in the walk's own loop
-// (M in registers takes half the time here, but 2 us of each of the three cases
-// above).
+// (M in registers takes half the time here, but up to 2 us of the cases above,
+// whose loop the compiler then schedules otherwise).
 //
 // A walk's last matrix may take the first one's place.  The CTA that ends such
 // a walk leaves it to this function, and waits until the CTA that began the
