@@ -1098,7 +1098,9 @@ cudaError_t join(const GroupNorm& A, int64_t samples, bool backward, cudaStream_
 template <typename K>
 cudaError_t launch_held(K k, const HeldPlan& h, GroupNorm A, cudaStream_t s) {
     if (h.bytes > kPlainBytes) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, h.bytes);
+        // the same for every size: the attribute is the kernel's, and another thread's smaller call
+        // may set it between this one's two steps
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldBytes);
         if (e != cudaSuccess) return e;
     }
     A.set = h.set;
