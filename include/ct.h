@@ -275,7 +275,8 @@ int ct_conv_transpose_nd_host(const void* x, const void* w, const void* bias,
  */
 typedef enum {
     CT_ACT_NONE = 0,
-    CT_ACT_RELU = 1,        /* max(v, 0) */
+    CT_ACT_RELU = 1,        /* max(v, 0); of NaN 0 after a convolution, NaN in
+                               the layers around it */
     CT_ACT_LEAKY_RELU = 2,  /* v >= 0 ? v : alpha * v */
     CT_ACT_SILU = 3,        /* v / (1 + exp(-v)) */
     CT_ACT_GELU = 4,        /* v * (1 + erf(v / sqrt(2))) / 2 */

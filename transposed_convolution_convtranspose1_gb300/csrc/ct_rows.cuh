@@ -141,10 +141,20 @@ __device__ __forceinline__ float sigmoid(float v) {
     }
 }
 
-// Activation (ct_activation codes) and its derivative at v.
+// max(v, 0); NaN stays NaN (a comparison would make it 0, and a group or a row
+// that holds one would look finite), in one instruction as well.
+__device__ __forceinline__ float relu(float v) {
+    float m;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// Activation (ct_activation codes) and its derivative at v; both are NaN where v
+// is (the slope of none is 1).
 template <int A, bool FAST>
 __device__ __forceinline__ float act_value(float v, float alpha) {
-    if constexpr (A == 3) return v * sigmoid<FAST>(v);
+    if constexpr (A == 1) return relu(v);
+    else if constexpr (A == 3) return v * sigmoid<FAST>(v);
     else if constexpr (A == 6) return sigmoid<FAST>(v);
     else return act_fixed<A>(v, alpha);
 }
@@ -175,11 +185,11 @@ __device__ __forceinline__ float2 act_value2(float2 v, float alpha) {
 template <int A, bool FAST>
 __device__ __forceinline__ void act_both(float v, float alpha, float& f, float& slope) {
     if constexpr (A == 1) {
-        f = v > 0.f ? v : 0.f;
-        slope = v > 0.f ? 1.f : 0.f;
+        f = relu(v);
+        slope = v <= 0.f ? 0.f : v > 0.f ? 1.f : v;
     } else if constexpr (A == 2) {
         f = v >= 0.f ? v : alpha * v;
-        slope = v >= 0.f ? 1.f : alpha;
+        slope = v >= 0.f ? 1.f : v < 0.f ? alpha : v;
     } else if constexpr (A == 3) {
         const float s = sigmoid<FAST>(v);
         f = v * s;
