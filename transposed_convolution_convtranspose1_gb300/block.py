@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -122,7 +123,7 @@ def _extent(t: torch.Tensor):
     if len(shape) == 2:
         return shape
     cols = shape[-1]
-    return (t.numel() // cols if cols else 0), cols
+    return (t.numel() // cols if cols else math.prod(shape[:-1])), cols
 
 
 def _like(t: torch.Tensor) -> torch.Tensor:
