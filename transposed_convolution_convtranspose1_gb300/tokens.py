@@ -312,8 +312,11 @@ def _in_place(p, rows, cols, stride, e) -> bool:
     return not p & 15 and (rows <= 1 or (stride >= cols and not stride * e & 15))
 
 
-def _weight_in_place(p, strides, C, F, e) -> bool:
-    return _in_place(p, C, F, strides[0], e) if strides[1] == 1 or F <= 1 else _in_place(p, F, C, strides[1], e)
+def _weights_in_place(pg, sg, pu, su, C, F, f_dense, e) -> bool:
+    """The same of both weights, read along the axis that is dense in all of them and their gradients."""
+    if f_dense:
+        return _in_place(pg, C, F, sg[0], e) and _in_place(pu, C, F, su[0], e)
+    return _in_place(pg, F, C, sg[1], e) and _in_place(pu, F, C, su[1], e)
 
 
 @functools.lru_cache(maxsize=256)
@@ -343,7 +346,8 @@ def gated_projection(x: torch.Tensor, w_gate: torch.Tensor, w_up: Optional[torch
     code, e = dtype_code(x.dtype), x.element_size()
     y = torch.empty((*x.shape[:-1], F), dtype=x.dtype, device=x.device)
     sg, su, pg, pu = gate.stride(), up.stride(), gate.data_ptr(), up.data_ptr()
-    aligned = _in_place(px, rows, C, sx, e) and _weight_in_place(pg, sg, C, F, e) and _weight_in_place(pu, su, C, F, e)
+    f_dense = F <= 1 or sg[1] == su[1] == 1
+    aligned = _in_place(px, rows, C, sx, e) and _weights_in_place(pg, sg, pu, su, C, F, f_dense, e)
     nws = _projection_workspace_bytes(rows, C, F, code, 0, aligned, index)
     ws = torch.empty((nws,), dtype=torch.uint8, device=x.device) if nws else None
     _call(lib().ct_gated_projection_forward, index, px, sx, pg, _two(*sg), pu, _two(*su),
@@ -384,8 +388,9 @@ def gated_projection_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.T
         dg = like_weight(F) if "dw_gate" in need else None
         du = like_weight(F) if "dw_up" in need else None
     sdg, sdu = dg.stride() if dg is not None else (0, 0), du.stride() if du is not None else (0, 0)
-    aligned = (_in_place(px, rows, C, sx, e) and _in_place(pd, rows, F, sd, e) and _weight_in_place(gate.data_ptr(), sg, C, F, e)
-               and _weight_in_place(up.data_ptr(), su, C, F, e))
+    f_dense = F <= 1 or (sg[1] == su[1] == 1 and (dg is None or sdg[1] == 1) and (du is None or sdu[1] == 1))
+    aligned = (_in_place(px, rows, C, sx, e) and _in_place(pd, rows, F, sd, e)
+               and _weights_in_place(gate.data_ptr(), sg, up.data_ptr(), su, C, F, f_dense, e))
     nws = _projection_workspace_bytes(rows, C, F, code, 1, aligned, index)
     ws = torch.empty((nws,), dtype=torch.uint8, device=dev) if nws else None
     _call(lib().ct_gated_projection_backward, index, pd, sd, px, sx, gate.data_ptr(), _two(*sg), up.data_ptr(), _two(*su),
