@@ -709,10 +709,16 @@ int ct_gated_projection_backward(const void* dy, int64_t dy_stride, const void* 
                                  void* stream);
 
 /*
- * Workspace of the two calls (backward: 0 or 1).  aligned != 0 says that x, the
- * weights and dy have pointers and row strides that are multiples of 16 bytes,
- * and rows that do not overlap; other calls need room for aligned copies.
+ * Workspace of the two calls (backward: 0 or 1).  "In place" is said of a matrix
+ * whose pointer and row stride are multiples of 16 bytes and whose rows do not
+ * overlap; a single row has no stride.  aligned is a sum of what is known:
+ *   CT_GATED_ALIGNED: x, the weights and dy are in place (other calls need room
+ *     for aligned copies);
+ *   CT_GATED_WEIGHTS_F or CT_GATED_WEIGHTS_C: the weights are, with their F or
+ *     their C axis as the dense one (F where both are): a forward call of a few
+ *     rows then needs no workspace, whatever x is like.
  */
+enum { CT_GATED_ALIGNED = 1, CT_GATED_WEIGHTS_F = 2, CT_GATED_WEIGHTS_C = 4 };
 int ct_gated_projection_workspace_bytes(int64_t rows, int64_t C, int64_t F,
                                         int dtype, int backward, int aligned,
                                         size_t* bytes);

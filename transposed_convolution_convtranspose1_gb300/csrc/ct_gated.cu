@@ -395,7 +395,10 @@ extern "C" int ct_gated_projection_workspace_bytes(int64_t rows, int64_t C, int6
     if (!bytes) return report_error(CT_ERR_NULL, "bytes is NULL");
     const int rc = check_problem(rows, C, F, dtype);
     if (rc != CT_OK) return rc;
-    *bytes = workspace_bytes_of(rows, C, F, dtype, backward, aligned);
+    // few rows go past the tensor cores (few() above), which needs none
+    const bool none = !backward && (((aligned & CT_GATED_WEIGHTS_F) && gated_few_fits(rows, C, F, true, dtype)) ||
+                                    ((aligned & CT_GATED_WEIGHTS_C) && gated_few_fits(rows, C, F, false, dtype)));
+    *bytes = none ? 0 : workspace_bytes_of(rows, C, F, dtype, backward, aligned & CT_GATED_ALIGNED);
     return CT_OK;
 }
 

@@ -292,6 +292,9 @@ def rotary_autograd(q, k, positions, table: RotaryTable, interleaved: bool = Fal
 
 # ---- gated projection ------------------------------------------------------
 
+_ALIGNED, _WEIGHTS_F, _WEIGHTS_C = 1, 2, 4  # CT_GATED_*: what the workspace query is told
+
+
 def _weights(x, w_gate, w_up):
     """(gate, up) as [C, F] matrices; w_up None: w_gate holds both, [C, 2F]."""
     if w_up is None:
@@ -347,7 +350,9 @@ def gated_projection(x: torch.Tensor, w_gate: torch.Tensor, w_up: Optional[torch
     y = torch.empty((*x.shape[:-1], F), dtype=x.dtype, device=x.device)
     sg, su, pg, pu = gate.stride(), up.stride(), gate.data_ptr(), up.data_ptr()
     f_dense = F <= 1 or sg[1] == su[1] == 1
-    aligned = _in_place(px, rows, C, sx, e) and _weights_in_place(pg, sg, pu, su, C, F, f_dense, e)
+    aligned = 0
+    if _weights_in_place(pg, sg, pu, su, C, F, f_dense, e):
+        aligned = (_WEIGHTS_F if f_dense else _WEIGHTS_C) | (_ALIGNED if _in_place(px, rows, C, sx, e) else 0)
     nws = _projection_workspace_bytes(rows, C, F, code, 0, aligned, index)
     ws = torch.empty((nws,), dtype=torch.uint8, device=x.device) if nws else None
     _call(lib().ct_gated_projection_forward, index, px, sx, pg, _two(*sg), pu, _two(*su),
@@ -389,8 +394,8 @@ def gated_projection_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.T
         du = like_weight(F) if "dw_up" in need else None
     sdg, sdu = dg.stride() if dg is not None else (0, 0), du.stride() if du is not None else (0, 0)
     f_dense = F <= 1 or (sg[1] == su[1] == 1 and (dg is None or sdg[1] == 1) and (du is None or sdu[1] == 1))
-    aligned = (_in_place(px, rows, C, sx, e) and _in_place(pd, rows, F, sd, e)
-               and _weights_in_place(gate.data_ptr(), sg, up.data_ptr(), su, C, F, f_dense, e))
+    aligned = _ALIGNED if (_in_place(px, rows, C, sx, e) and _in_place(pd, rows, F, sd, e)
+                           and _weights_in_place(gate.data_ptr(), sg, up.data_ptr(), su, C, F, f_dense, e)) else 0
     nws = _projection_workspace_bytes(rows, C, F, code, 1, aligned, index)
     ws = torch.empty((nws,), dtype=torch.uint8, device=dev) if nws else None
     _call(lib().ct_gated_projection_backward, index, pd, sd, px, sx, gate.data_ptr(), _two(*sg), up.data_ptr(), _two(*su),
