@@ -15,6 +15,7 @@ from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from .block import (_activation, _call, _check_weight, _dense, _extent, _heads, _index_of, _like, _on, _rows, _strides)
 from .ct import CT_ERR_DTYPE, CT_ERR_GROUPS, CT_ERR_PARAM, CT_ERR_SHAPE, CtError, _check, dtype_code, lib
@@ -218,7 +219,9 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
     positions [B, T, axes] or [T, axes] (int32, int64, or float32 between grid
     points).  Pair i is (i, i + pairs), or (2i, 2i + 1) with `interleaved`; what
     follows the pairs is copied.  `inverse` turns back (the gradient).  Returns
-    (q, k) turned, in `out` (a pair, which may be q and k themselves) if given.
+    (q, k) turned, in `out` (a pair, which may be q and k themselves) if given;
+    autograd does not see that, so `out` may not ask for a gradient where
+    gradients are recorded.
     """
     if stream is not None:
         with _on(stream, q):
@@ -253,12 +256,16 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
         qo, ko = out
         if (ko is None) != (k is None):
             raise CtError(CT_ERR_SHAPE, "out has a second entry exactly where there is k")
+        if torch.is_grad_enabled() and (qo.requires_grad or (ko is not None and ko.requires_grad)):
+            raise CtError(CT_ERR_PARAM, "out may not ask for a gradient: call rotary_autograd, or under torch.no_grad()")
         pqo, sqo = _heads(qo, (B, T, Hq, D), dt)
         pko, sko = _heads(ko, (B, T, Hk, D), dt)
         index = _index_of(q, k, positions, table.turns, qo, ko)
     _call(lib().ct_rotary, index, pq, sq, pk, sk, pqo, sqo, pko, sko, positions.data_ptr(), sp,
           _POSITION_DTYPE[positions.dtype], _dense(table.turns), _sections(table.sections), axes, B, T, Hq, Hk, D,
           int(interleaved), int(inverse), dtype_code(dt))
+    if out is not None:  # a backward pass that kept them finds out
+        increment_version(qo if ko is None else (qo, ko))
     return qo, ko
 
 
