@@ -1034,7 +1034,8 @@ struct Plan {
 Plan plan(int64_t B, int64_t S, int64_t C, int64_t G, int dtype, int backward, int sm) {
     Plan p;
     const int64_t sample = std::max<int64_t>(1, S * C * (dtype == CT_F32 ? 4 : 2) * (backward ? 2 : 1));
-    p.range = std::min<int64_t>({std::max<int64_t>(1, kRangeBytes / sample), std::max<int64_t>(B, 1), 32768});
+    // a grid's z has 65535 at most, the join's x (a block for each group) 2^31 - 1
+    p.range = std::min<int64_t>({std::max<int64_t>(1, kRangeBytes / sample), std::max<int64_t>(B, 1), 32768, 2147483647 / G});
     // what is resident at once, at least 16 positions a chunk
     const int64_t want = std::max<int64_t>(1, (backward ? kBwdBlocks : kBlocks) * sm / p.range);
     const int64_t most = (S + 15) / 16;
