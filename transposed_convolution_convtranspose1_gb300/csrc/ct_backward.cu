@@ -1062,8 +1062,8 @@ cudaError_t launch_dx_t(const BwdArgs& a, const BwdPlan& pl, cudaStream_t stream
     const int64_t gz = (rows + gy - 1) / gy;
     if (gz > 65535) return cudaErrorInvalidConfiguration;
     if (pl.dx_smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(bwd_dx_kernel<T, ICB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)pl.dx_smem);
+        static SharedLimit limit;
+        cudaError_t e = limit.allow((const void*)bwd_dx_kernel<T, ICB>, pl.dx_smem);
         if (e != cudaSuccess) return e;
     }
     bwd_dx_kernel<T, ICB><<<dim3((unsigned)gx, (unsigned)gy, (unsigned)gz), kDxThreads, pl.dx_smem, stream>>>(
@@ -1078,7 +1078,8 @@ cudaError_t launch_dwg_v(const BwdArgs& a, const DwgGeom& G, size_t smem, cudaSt
     auto k = bwd_dw_grouped_kernel<T, ICT, KN, ROWS>;
     constexpr int threads = kDwgC * (kDwgC / ICT) * 32;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static SharedLimit limit;
+        cudaError_t e = limit.allow((const void*)k, smem);
         if (e != cudaSuccess) return e;
     }
     k<<<(unsigned)G.n_blocks, threads, smem, stream>>>(a, G);

@@ -146,8 +146,8 @@ cudaError_t launch_gather_t(const GatherArgs& a, cudaStream_t stream, int sm_cou
     dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)gz);
     if (use_smem) {
         if (slab > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(gather_kernel<T, OCB, true>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)slab);
+            static SharedLimit limit;
+            cudaError_t e = limit.allow((const void*)gather_kernel<T, OCB, true>, slab);
             if (e != cudaSuccess) return e;
         }
         prof_begin(prof, stream);

@@ -417,8 +417,8 @@ bool make_plan(const Problem& p, GroupedPlan* pl) {
 template <typename T, int SW, int COG, int CIGP>
 cudaError_t launch_staged(const GroupedParams& P, int64_t blocks, size_t smem, cudaStream_t stream) {
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(grouped_staged_kernel<T, SW, COG, CIGP>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static SharedLimit limit;
+        cudaError_t e = limit.allow((const void*)grouped_staged_kernel<T, SW, COG, CIGP>, smem);
         if (e != cudaSuccess) return e;
     }
     grouped_staged_kernel<T, SW, COG, CIGP><<<(unsigned)blocks, kGrpWarps * 32, smem, stream>>>(P);

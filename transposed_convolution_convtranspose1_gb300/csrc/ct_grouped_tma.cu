@@ -365,8 +365,8 @@ cudaError_t launch_grouped_tma(const Problem& p, const void* x, const void* w, c
     if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
     const size_t smem = pl.smem;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(grouped_tma_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static SharedLimit limit;
+        cudaError_t e = limit.allow((const void*)grouped_tma_kernel, smem);
         if (e != cudaSuccess) return e;
     }
     grouped_tma_kernel<<<(unsigned)blocks, kGW * 32, smem, stream>>>(P);

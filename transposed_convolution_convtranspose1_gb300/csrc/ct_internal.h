@@ -7,6 +7,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -71,6 +72,26 @@ struct DeviceInfo {
     size_t smem_optin;
 };
 cudaError_t device_info(DeviceInfo* out);
+
+// A kernel's limit of dynamic shared memory, one object for each kernel.  The
+// limit belongs to the function on a device, whichever thread launches it: set to
+// one call's own size it could be lowered by another thread's smaller call before
+// the launch.  Here it only rises (it allows, and reserves nothing).
+struct SharedLimit {
+    std::mutex mu;
+    size_t most[64] = {};  // by device
+    cudaError_t allow(const void* kernel, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lock(mu);
+        size_t& m = most[dev & 63];
+        const size_t want = bytes > m ? bytes : m;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
+        if (e == cudaSuccess) m = want;
+        return e;
+    }
+};
 
 // Optional per-call profiling: events recorded on the launching stream just
 // before and just after the route's dominant kernel, and a count of the
