@@ -252,7 +252,15 @@ __device__ __forceinline__ void tmem_ld_wait() {
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // cuTensorMapEncodeTiled from the driver (no link-time dependency on libcuda).
+// It fails in a thread that has no context yet, and a call may be its thread's
+// first use of the GPU: the runtime binds the current device's here (allowed in
+// a capture, too).
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    thread_local bool bound = false;
+    if (!bound) {
+        int dev = 0;
+        bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+    }
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
