@@ -38,6 +38,7 @@
 #include "ct_gated.h"
 #include "ct_internal.h"
 #include "ct_rows.cuh"
+#include "ct_settle.h"
 #include "ct_tcgen05.cuh"
 
 namespace ct {
@@ -106,6 +107,14 @@ __device__ __forceinline__ uint32_t at_first(uint32_t addr) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
+}
+// Into the other SM's copy of a shared variable.
+__device__ __forceinline__ void put_other(uint32_t addr, uint32_t other, uint32_t v) {
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(addr), "r"(other), "r"(v) : "memory");
+}
+// Bytes that were announced and will not land.
+__device__ __forceinline__ void complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -343,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
     __shared__ uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], acc_full[2], acc_empty[2], dy_bar[kEpiWarps], done_bar;
     __shared__ uint32_t tmem_base_slot;
     __shared__ volatile int abort_flag;
+    // uses of the ring that the producers of A and B issued; the other SM's, and whether it gave up
+    __shared__ uint32_t sent[2], other_sent[2], other_abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
@@ -350,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
+        other_abort = 0;
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 2);
             mbar_init(smem_u32(&empty_bar[s]), 1);
@@ -448,12 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
                 }
             }
         }
-        if (rank == 0 && lane == 0) {
-            // every copy issued (on a pair: by both) must land before the CTAs exit,
-            // also where another role gives up after the last of them
-            const uint32_t from = issued > (uint32_t)L::kStages ? issued - L::kStages : 0;
-            for (uint32_t k = from; k < issued; ++k) mbar_drain(smem_u32(&full_bar[k % L::kStages]), (k / L::kStages) & 1);
-        }
+        if (lane == 0) sent[is_b] = issued;
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
@@ -653,14 +660,34 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) {
-        // after a give-up the two SMs may have issued different numbers of copies, and the
-        // barriers drained above know only the first one's: leave the others a millisecond to land
-        if (abort_flag) {
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 1000000ull) {
+        if (threadIdx.x == 0) {
+            if (rank == 1) {
+                put_other(smem_u32(&other_sent[0]), 0, sent[0]);
+                put_other(smem_u32(&other_sent[1]), 0, sent[1]);
+            }
+            if (abort_flag) put_other(smem_u32(&other_abort), rank ^ 1, 1);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    if (abort_flag || (CG == 2 && other_abort)) {
+        // every copy issued must land before an SM exits (without a give-up the MMAs have waited
+        // for all); where the producers stopped at different uses, the barriers get what they lack
+        if (rank == 0 && threadIdx.x == 0) {
+            uint32_t n = max(sent[0], sent[1]);
+            if constexpr (CG == 2) n = max(n, max(other_sent[0], other_sent[1]));
+            for (uint32_t k = unsettled_from(n, L::kStages); k < n; ++k) {
+                const uint32_t bar = smem_u32(&full_bar[k % L::kStages]);
+                for (int i = 0; i < 2; ++i) {
+                    const Owed o = owed(k, sent[i], CG == 2 ? other_sent[i] : 0, CG == 2, i ? L::kStage - kBlock : kBlock);
+                    if (o.arrive) mbar_expect_tx(bar, o.announce);
+                    if (o.absent) complete_tx(bar, o.absent);
+                }
+                mbar_drain(bar, (k / L::kStages) & 1);
             }
         }
-        cluster_sync();
+        __syncthreads();
+        if constexpr (CG == 2) cluster_sync();
     }
     tc_fence_after();
     if (warp == 1) {
