@@ -2,9 +2,9 @@
 //
 // With a few rows the weights are nearly all there is to read, and each is
 // used that often: plain fp32 multiply-adds keep up with memory (at 6.7 TB/s an SM
-// gets about 12 16-bit weights a cycle; four rows make 46 multiply-adds of them).  No tiles, no copies: weights go
-// from global memory to registers, 8 or 16 bytes an access, fp32 ones as they
-// are.  Each result is summed in a fixed order.
+// gets about 12 16-bit weights a cycle; four rows make 46 multiply-adds of them).  No
+// tiles, no copies: weights go from global memory to registers, 16 bytes an access,
+// fp32 ones as they are.  Each result is summed in a fixed order.
 //
 // F dense: a block takes 128 or 256 columns; its warps take every eighth row of W in
 // its share of C, blocks of a cluster share C and add up through distributed
@@ -33,16 +33,15 @@ using namespace rows;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSlice = 512;     // of C in shared memory at a time
 
-// F dense: columns of a thread (its 4 R or 8 R pairs of sums stay in registers),
-// rows of W on their way, and the shared memory of a block.
-template <typename T, int R>
-constexpr int few_columns() { return sizeof(T) == 2 && R <= 4 ? 8 : 4; }
-template <typename T, int R>
-constexpr int few_depth() { return few_columns<T, R>() * sizeof(T) == 8 ? 12 : 6; }
+// F dense: columns of a thread (R pairs of sums for each stay in registers), rows of
+// W on their way, and the shared memory of a block.
+template <typename T>
+constexpr int few_columns() { return 16 / (int)sizeof(T); }
+constexpr int kDepth = 6;
 template <typename T, int R>
 constexpr int few_bytes() {
-    constexpr int own = 2 * R * 32 * few_columns<T, R>() * 4;
-    constexpr int a = kSlice * R * 4 + few_depth<T, R>() * 2 * kThreads * few_columns<T, R>() * (int)sizeof(T), b = kWarps * own;
+    constexpr int own = 2 * R * 32 * few_columns<T>() * 4;
+    constexpr int a = kSlice * R * 4 + kDepth * 2 * kThreads * 16, b = kWarps * own;
     return (a > b ? a : b) + own;
 }
 
@@ -70,13 +69,6 @@ __device__ __forceinline__ float of_block(const float* p, unsigned rank) {
     return v;
 }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_bytes(void* to, const void* from) {
-    if constexpr (BYTES == 16) copy16(to, from, true);
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from), "n"(BYTES) : "memory");
-}
-
 template <bool FAST>
 __device__ __forceinline__ float gated(float g, float u, int act, float alpha) {
     float v[1] = {g};
@@ -97,8 +89,7 @@ __device__ __forceinline__ void stage_x(const Few& A, float* xs, int c0, int n) 
 template <typename T, int R>
 __global__ void __launch_bounds__(kThreads) gated_few_f(Few A) {
     extern __shared__ __align__(16) float shared[];
-    constexpr int V = few_columns<T, R>(), kColumns = 32 * V, kBytes = V * (int)sizeof(T);
-    constexpr int kDepth = few_depth<T, R>(), kOwn = 2 * R * kColumns;
+    constexpr int V = few_columns<T>(), kColumns = 32 * V, kOwn = 2 * R * kColumns;
     // x [slice][R] and the slots; afterwards the warps' sums [warps][2][R][columns]
     float* const xs = shared;
     char* const slots = reinterpret_cast<char*>(shared + kSlice * R);
@@ -130,8 +121,8 @@ __global__ void __launch_bounds__(kThreads) gated_few_f(Few A) {
         int asked = 0;
         const auto ask = [&](int slot) {
             if (asked < mine_n) {
-                copy_bytes<kBytes>(slots + (2 * slot * kThreads + threadIdx.x) * kBytes, pg);
-                copy_bytes<kBytes>(slots + ((2 * slot + 1) * kThreads + threadIdx.x) * kBytes, pu);
+                copy16(slots + (2 * slot * kThreads + threadIdx.x) * 16, pg, true);
+                copy16(slots + ((2 * slot + 1) * kThreads + threadIdx.x) * 16, pu, true);
                 pg += dg;
                 pu += du;
             }
@@ -147,8 +138,8 @@ __global__ void __launch_bounds__(kThreads) gated_few_f(Few A) {
                 copies_wait<kDepth - 1>();
                 if (i + k < mine_n) {
                     Vec<T, V> a, b;
-                    a.load(reinterpret_cast<const T*>(slots + (2 * k * kThreads + threadIdx.x) * kBytes));
-                    b.load(reinterpret_cast<const T*>(slots + ((2 * k + 1) * kThreads + threadIdx.x) * kBytes));
+                    a.load(reinterpret_cast<const T*>(slots + (2 * k * kThreads + threadIdx.x) * 16));
+                    b.load(reinterpret_cast<const T*>(slots + ((2 * k + 1) * kThreads + threadIdx.x) * 16));
                     float p[V], q[V], x[R];
                     a.values(p);
                     b.values(q);
@@ -290,7 +281,7 @@ cudaError_t launch_r(const Few& A, bool f_dense, int sm_count, cudaStream_t s) {
         gated_few_c<T, R><<<(unsigned)((A.F + n - 1) / n), kThreads, R * kSlice * 4, s>>>(A);
         return cudaGetLastError();
     }
-    constexpr int columns = 32 * few_columns<T, R>();
+    constexpr int columns = 32 * few_columns<T>();
     const int strips = (A.F + columns - 1) / columns;
     // two blocks an SM, 16 rows of W a block at least
     int ranks = 1;
