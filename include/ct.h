@@ -650,7 +650,8 @@ typedef enum { CT_POS_I32 = 0, CT_POS_I64 = 1, CT_POS_F32 = 2 } ct_position_dtyp
  *     same for every sequence).
  * Cosines, sines and products are fp32, rounded once.
  * Errors: CT_ERR_DTYPE, CT_ERR_SHAPE, CT_ERR_PARAM (axes, sections, position
- * type), CT_ERR_NULL, CT_ERR_ALIGN, CT_ERR_TOO_LARGE (D > 1024), CT_ERR_CUDA.
+ * type), CT_ERR_NULL, CT_ERR_ALIGN, CT_ERR_TOO_LARGE (D > 1024, Hq + Hk > 65536, B * T
+ * > 2^31 - 1), CT_ERR_CUDA.
  */
 #define CT_ROTARY_MAX_AXES 4
 int ct_rotary(const void* q, const int64_t* q_strides, const void* k,

@@ -28,8 +28,10 @@
 // Bound by shared-memory bandwidth: a block of K (64) writes 32 KB into an SM's
 // shared memory and its MMAs read about 48 KB of it, some 640 cycles at 128 bytes
 // a cycle, where the MMAs themselves take 512; the tensor pipe is active 81% of
-// the cycles (16384 x 1024 x 4096 bf16 with silu: 151 us, 1820 TFLOP/s, 94% of the
-// measured product rate; long runs meet the power limit: 176 us).  A wait on a
+// the cycles.  16384 x 1024 x 4096 bf16 with silu, back to back for a second, where the
+// power limit lowers the clock: 174 us, 1580 TFLOP/s, 82% of the measured product rate
+// (91% of the sustained one); the first calls after a pause: 151 us, 94%.  Its
+// gradients: 555 us, 77% (85%); 475 us after a pause.  A wait on a
 // barrier takes an issuing warp 100 cycles, a copy 110, an expected count 65: one
 // producer warp for both operands was slower than the MMAs (650 cycles a block,
 // 190 us), one for each is not.
@@ -544,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm(const __grid_constant_
             const int row = tile.m + (int)rank * 128 + q * 32;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             // fp32: the sums of a chunk of K are added up here, rounded to nearest.  The tensor core
-            // drops what it shifts out of its sums; over all of K that would add up.
+            // drops what it shifts out of its sums; over all of K that would add up.  128 sums a
+            // thread leave few registers: 168 and about 1 KB of spills where dg and du follow, 40
+            // bytes in the forward product, none in the others.
             float sum[kWide ? 128 : 1];
             if constexpr (kWide) {
 #pragma unroll
