@@ -74,3 +74,28 @@ def test_a_first_call(name):
     assert rc[0][0] == ct.CT_OK, rc
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_context_of_the_callers_stays_current():
+    """A query that looks at the tensor-map route, in a thread whose current context is not the runtime's; nothing is launched there."""
+    torch.zeros(1, device="cuda")
+    cu = ctypes.CDLL("libcuda.so.1")
+    found = []
+
+    def work():
+        mine, now = ctypes.c_void_p(), ctypes.c_void_p()
+        code = cu.cuCtxCreate_v2(ctypes.byref(mine), 0, 0)
+        if code:
+            found.append(f"no second context here (driver status {code})")
+            return
+        name = ctb.ct_conv_transpose_kernel(1, 16, 16, (4, 16, 32), (2, 4, 4), 2, groups=2)
+        cu.cuCtxGetCurrent(ctypes.byref(now))
+        found.append((name, now.value == mine.value))
+        cu.cuCtxDestroy_v2(mine)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    if isinstance(found[0], str):
+        pytest.skip(found[0])
+    assert found[0][0].startswith("grouped") and found[0][1]

@@ -251,26 +251,28 @@ __device__ __forceinline__ void tmem_ld_wait() {
 
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// cuTensorMapEncodeTiled from the driver (no link-time dependency on libcuda).
-// It fails in a thread that has no context yet, and a call may be its thread's
-// first use of the GPU: the runtime binds the current device's here (allowed in
-// a capture, too).
+// A driver function without a link-time dependency on libcuda; null where there is none.
+inline void* driver_fn(const char* name, unsigned version) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion(name, &f, version, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f : nullptr;
+}
+
+// cuTensorMapEncodeTiled.  It fails in a thread that has no context, and a call
+// may be its thread's first use of the GPU: the runtime binds the current device's
+// here (allowed in a capture, too).  A context that the caller has made current stays.
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    thread_local bool bound = false;
-    if (!bound) {
-        int dev = 0;
-        bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
-    }
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static PFN_cuCtxGetCurrent_v4000 current = nullptr;
     std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_fn("cuTensorMapEncodeTiled", 12000));
+        current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_fn("cuCtxGetCurrent", 4000));
     });
+    CUcontext c = nullptr;
+    int dev = 0;
+    if (current && (current(&c) != CUDA_SUCCESS || !c) && cudaGetDevice(&dev) == cudaSuccess) cudaSetDevice(dev);
     return fn;
 }
 
